@@ -1,0 +1,143 @@
+// decay_attn.h -- what the kernels of the head-decay linear attention share:
+// the problems of one call, how a sequence is cut into segments, and the walk
+// from a block to its segment.
+//
+// A problem is  o_t = c lambda^(t+1) q_t S0 + a sum_{s<=t} lambda^(t-s) (q_t . k_s) v_s
+// over scan positions t of a sequence, with the carried state
+//   S_t = lambda S_{t-1} + b k_t^T v_t.
+// The forward is one problem (a = c = scale, b = 1).  The backward is three of
+// the same form: dq from (dO, v, k) and S0^T in the forward's order; dv from
+// (k, q, dO) and dk from (v, dO, q) in the reversed order, where the state is the
+// adjoint one, starts from dS_final (transposed for dk) without the first lambda
+// ("lag"), and ends, times lambda, as dS0.
+//
+// A sequence is cut into segments of `seg` tokens, each walked by one block in
+// chunks.  With more than one segment per sequence a first kernel leaves every
+// segment's own state contribution (segment 0: with S0 in it), and the second
+// one joins those before its segment into the state it starts from.
+#pragma once
+#include <cuda_runtime.h>
+
+#include "dig_common.cuh"
+
+namespace dig {
+
+struct DecayProblem {
+  const void *q, *k, *v;
+  void* o;
+  long long qs, ks, vs;  // elements between tokens
+  const float* S0;       // NULL: zero
+  float* Sf;             // NULL: not wanted
+  int dk, dv;            // the problem's own (dq and dk exchange the call's)
+  int s0_t;              // S0 is stored [d_v][d_k]
+  int lag;
+  int mode;
+  float a, b, c;
+};
+
+struct DecayArgs {
+  DecayProblem p[3];
+  const float* g;  // [H] log decays
+  const int* cu;
+  const int* slots;
+  int n_slots;
+  int B, H, L, Hg, Wg;
+  int seg;        // tokens of a segment
+  int nps;        // segments of a sequence of L tokens (without cu)
+  float* segst;   // [problem][segment][H][D * D] segment states
+  long long segst_problem;  // elements between problems there
+  uint32_t* status;
+  unsigned long long spin_ns;
+};
+
+struct DecayUnit {
+  int b, i, nseg;  // sequence, segment of it, its segments
+  int first, len;  // the sequence's first row and length
+  int t0, n;       // the segment's first scan position and its tokens
+  int slot;        // state of the sequence, -1: none
+};
+
+// Row of scan position t of unit u's sequence.
+__device__ __forceinline__ int decay_row(const DecayArgs& a, const DecayUnit& u, int mode, int t) {
+  if (a.cu) return u.first + ((mode & 1) ? u.len - 1 - t : t);
+  return u.first + scan_to_grid(t, a.L, a.Hg, a.Wg, mode);
+}
+
+// Bounds of sequence b among the packed rows, forced into 0 .. L.
+__device__ __forceinline__ void decay_bounds(const DecayArgs& a, int b, int& lo, int& hi) {
+  lo = min(max(a.cu[b], 0), a.L);
+  hi = min(max(a.cu[b + 1], lo), a.L);
+}
+
+// The unit of segment slot `sidx` of the call; every lane of the calling warp
+// gets it.  False: the call has fewer segments.
+__device__ __forceinline__ bool decay_unit(const DecayArgs& a, int sidx, DecayUnit& u) {
+  const int lane = threadIdx.x & 31;
+  if (!a.cu) {
+    u.b = sidx / a.nps;
+    u.i = sidx - u.b * a.nps;
+    u.nseg = a.nps;
+    u.first = u.b * a.L;
+    u.len = a.L;
+  } else {
+    int base = 0;
+    bool found = false;
+    for (int b0 = 0; b0 < a.B && !found; b0 += 32) {
+      int lo = 0, hi = 0, ns = 0;
+      if (b0 + lane < a.B) {
+        decay_bounds(a, b0 + lane, lo, hi);
+        ns = max(1, (hi - lo + a.seg - 1) / a.seg);
+      }
+      int inc = ns;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, inc, m);
+        if (lane >= m) inc += x;
+      }
+      const unsigned has = __ballot_sync(0xFFFFFFFFu, base + inc > sidx);
+      if (has) {
+        const int src = __ffs(has) - 1;
+        u.b = b0 + src;
+        u.nseg = __shfl_sync(0xFFFFFFFFu, ns, src);
+        u.i = sidx - base - (__shfl_sync(0xFFFFFFFFu, inc, src) - u.nseg);
+        u.first = __shfl_sync(0xFFFFFFFFu, lo, src);
+        u.len = __shfl_sync(0xFFFFFFFFu, hi, src) - u.first;
+        found = true;
+      }
+      base += __shfl_sync(0xFFFFFFFFu, inc, 31);
+    }
+    if (!found) return false;
+  }
+  u.t0 = u.i * a.seg;
+  u.n = min(a.seg, u.len - u.t0);
+  u.slot = u.b;
+  if (a.slots) {
+    u.slot = a.slots[u.b];
+    bool bad = u.slot >= a.n_slots;
+    for (int j = lane; j < u.b && u.slot >= 0; j += 32) bad |= a.slots[j] == u.slot;
+    if (__any_sync(0xFFFFFFFFu, bad)) {
+      u.slot = -1;
+      if (lane == 0) set_status(a.status, DIG_ERR_INVALID_ARGUMENT);
+    }
+  }
+  return true;
+}
+
+// Reports offsets that do not ascend within 0 .. L (one warp of the call does this).
+__device__ __forceinline__ void decay_check_offsets(const DecayArgs& a) {
+  for (int b = threadIdx.x & 31; b < a.B; b += 32)
+    if (a.cu[b] < 0 || a.cu[b + 1] < a.cu[b] || a.cu[b + 1] > a.L) set_status(a.status, DIG_ERR_INVALID_ARGUMENT);
+}
+
+// lambda^i = hi + lo for a whole i >= 0, from the log decay as given (lambda^0 = 1 also for lambda = 0).
+__device__ __forceinline__ float2 decay_pow(float g, long long i) {
+  const double p = i == 0 ? 1.0 : exp(static_cast<double>(g) * static_cast<double>(i));
+  const float hi = static_cast<float>(p);
+  return make_float2(hi, isfinite(hi) ? static_cast<float>(p - hi) : 0.f);
+}
+
+// Launches of the two passes (states: only where a sequence has more than one segment).
+cudaError_t launch_decay_f32(const DecayArgs& a, int nprob, int nseg_total, bool multi, int D, int dtype, int out_dtype,
+                             cudaStream_t s);
+
+}  // namespace dig

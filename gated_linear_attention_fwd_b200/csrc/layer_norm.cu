@@ -1,0 +1,497 @@
+// layer_norm.cu -- layer norm over rows of D values and its backward
+// (slide eq. (10), "LN"):
+//   y  = (x - mean) rstd w + b,  rstd = 1 / sqrt(var + eps)
+//   xh = (x - mean) rstd,  a = dy w,
+//   dx = rstd (a - mean(a) - xh mean(a xh)),  dw = sum_rows dy xh,  db = sum_rows dy
+// Both are memory-bound: one read of x (and dy), one write of y (dx).  A row is
+// held in the registers of TPR threads (a warp up to 1024 values, then 128 or
+// 256 threads), so the variance is the two-pass one at no extra traffic; rows
+// wider than 8192 values are re-read from cache.  All sums are fp32.  The weight
+// gradients are summed per thread over the block's rows, then over the block's
+// rows of threads, and the blocks' partial rows by a second kernel, all in a
+// fixed order (no atomics: the same bits from run to run).
+#include <cuda_bf16.h>
+
+#include "../../include/dig.h"
+#include "dig_common.cuh"
+#include "sm100.cuh"
+
+namespace dig {
+
+void set_last_error(const char* msg);  // dig_api.cu
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxBlocks = 296;  // blocks of the backward: two per SM, one partial row of dw and db each
+
+// V consecutive elements as fp32 (V * sizeof(T) = 16, or V = 1).
+template <typename T, int V>
+__device__ __forceinline__ void ld_vec(const T* p, float* f) {
+  if constexpr (V == 1) {
+    f[0] = static_cast<float>(*p);
+  } else if constexpr (sizeof(T) == 2) {
+    static_assert(V == 8, "16-byte vectors");
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 u = __ldg(reinterpret_cast<const float4*>(p + i));
+      f[i] = u.x, f[i + 1] = u.y, f[i + 2] = u.z, f[i + 3] = u.w;
+    }
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void st_vec(T* p, const float* f) {
+  if constexpr (V == 1) {
+    if constexpr (sizeof(T) == 2) *p = __float2bfloat16_rn(f[0]);
+    else *p = f[0];
+  } else if constexpr (sizeof(T) == 2 && V == 8) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                              pack_bf16x2(f[6], f[7]));
+  } else {
+    store_row<V>(p, f);
+  }
+}
+
+// Sum over the TPR threads of a row; every thread gets it.  `red` holds two sets
+// of one float per warp for rows of several warps (TPR a multiple of 32 there),
+// used in turn so that one barrier per sum is enough.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* red, int& turn) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+  if constexpr (TPR > 32) {
+    static_assert(TPR == kThreads || kThreads % TPR == 0, "whole rows per block");
+    const int warp = threadIdx.x >> 5;
+    float* r = red + turn * (kThreads / 32);
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) r[warp] = v;
+    __syncthreads();
+    const int w0 = warp / (TPR / 32) * (TPR / 32);
+    v = r[w0];
+#pragma unroll
+    for (int i = 1; i < TPR / 32; ++i) v += r[w0 + i];
+  }
+  return v;
+}
+
+struct LnArgs {
+  const void* x;
+  long long x_stride;
+  const float *w, *b;
+  float eps;
+  void* y;
+  float *mean, *rstd;
+  long long rows;
+  int D;
+};
+
+// Rows in registers: NV vectors of V values per thread, TPR threads per row.
+template <typename T, typename TO, int V, int NV, int TPR>
+__global__ void __launch_bounds__(kThreads) ln_fwd_kernel(const LnArgs a) {
+  __shared__ float red[2 * kThreads / 32];
+  constexpr int RPB = kThreads / TPR;
+  const int tr = threadIdx.x % TPR;
+  int turn = 0;
+  const T* x = static_cast<const T*>(a.x);
+  TO* y = static_cast<TO*>(a.y);
+  const float inv_d = 1.f / a.D;
+  griddep_wait();
+  griddep_launch_dependents();
+  // every thread of a block takes the same number of steps (barriers in row_sum)
+  for (long long r0 = (long long)blockIdx.x * RPB; r0 < a.rows; r0 += (long long)gridDim.x * RPB) {
+    const long long row = r0 + threadIdx.x / TPR;
+    const bool on = row < a.rows;
+    float f[NV * V];
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * TPR + tr) * V;
+      if (on && c < a.D) ld_vec<T, V>(x + row * a.x_stride + c, f + i * V);
+      else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[i * V + e] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NV * V; ++i) s += f[i];
+    const float mean = row_sum<TPR>(s, red, turn) * inv_d;
+    float q = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if ((i * TPR + tr) * V < a.D) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          f[i * V + e] -= mean;
+          q = fmaf(f[i * V + e], f[i * V + e], q);
+        }
+      }
+    }
+    const float rstd = rsqrtf(row_sum<TPR>(q, red, turn) * inv_d + a.eps);
+    if (!on) continue;
+    if (tr == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * TPR + tr) * V;
+      if (c >= a.D) continue;
+      float w[V], b[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) w[e] = 1.f, b[e] = 0.f;
+      if (a.w) ld_vec<float, V>(a.w + c, w);
+      if (a.b) ld_vec<float, V>(a.b + c, b);
+#pragma unroll
+      for (int e = 0; e < V; ++e) w[e] = fmaf(f[i * V + e] * rstd, w[e], b[e]);
+      st_vec<TO, V>(y + row * a.D + c, w);
+    }
+  }
+}
+
+// Rows of any width, one block each, re-read from cache for the second and third pass.
+template <typename T, typename TO>
+__global__ void __launch_bounds__(kThreads) ln_fwd_wide_kernel(const LnArgs a) {
+  __shared__ float red[2 * kThreads / 32];
+  int turn = 0;
+  const float inv_d = 1.f / a.D;
+  griddep_wait();
+  griddep_launch_dependents();
+  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    TO* y = static_cast<TO*>(a.y) + row * a.D;
+    float s = 0.f;
+    for (int c = threadIdx.x; c < a.D; c += kThreads) s += static_cast<float>(x[c]);
+    const float mean = row_sum<kThreads>(s, red, turn) * inv_d;
+    float q = 0.f;
+    for (int c = threadIdx.x; c < a.D; c += kThreads) {
+      const float d = static_cast<float>(x[c]) - mean;
+      q = fmaf(d, d, q);
+    }
+    const float rstd = rsqrtf(row_sum<kThreads>(q, red, turn) * inv_d + a.eps);
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    for (int c = threadIdx.x; c < a.D; c += kThreads) {
+      const float v = fmaf((static_cast<float>(x[c]) - mean) * rstd, a.w ? a.w[c] : 1.f, a.b ? a.b[c] : 0.f);
+      st_vec<TO, 1>(y + c, &v);
+    }
+  }
+}
+
+struct LnBwdArgs {
+  const void* x;
+  long long x_stride;
+  const float *w, *mean, *rstd;
+  const void* dy;
+  void* dx;
+  float *pw, *pb;  // partial rows of dw and db, [blocks][D]; NULL: not wanted
+  long long rows;
+  int D;
+};
+
+template <typename T, typename TO, int V, int NV, int TPR>
+__global__ void __launch_bounds__(kThreads) ln_bwd_kernel(const LnBwdArgs a) {
+  __shared__ float red[2 * kThreads / 32];
+  extern __shared__ float part[];  // [RPB][D], only for RPB > 1
+  constexpr int RPB = kThreads / TPR;
+  const int tr = threadIdx.x % TPR, rb = threadIdx.x / TPR;
+  int turn = 0;
+  const T* x = static_cast<const T*>(a.x);
+  const T* dy = static_cast<const T*>(a.dy);
+  TO* dx = static_cast<TO*>(a.dx);
+  const float inv_d = 1.f / a.D;
+  float gw[NV * V], gb[NV * V];
+#pragma unroll
+  for (int i = 0; i < NV * V; ++i) gw[i] = gb[i] = 0.f;
+  griddep_wait();
+  griddep_launch_dependents();
+  for (long long r0 = (long long)blockIdx.x * RPB; r0 < a.rows; r0 += (long long)gridDim.x * RPB) {
+    const long long row = r0 + rb;
+    const bool on = row < a.rows;
+    float xh[NV * V], g[NV * V];
+    const float mean = on ? a.mean[row] : 0.f, rstd = on ? a.rstd[row] : 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * TPR + tr) * V;
+      if (on && c < a.D) {
+        ld_vec<T, V>(x + row * a.x_stride + c, xh + i * V);
+        ld_vec<T, V>(dy + row * a.D + c, g + i * V);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) xh[i * V + e] = mean, g[i * V + e] = 0.f;
+      }
+    }
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * TPR + tr) * V;
+      float w[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) w[e] = 1.f;
+      if (a.w && c < a.D) ld_vec<float, V>(a.w + c, w);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const int n = i * V + e;
+        xh[n] = (xh[n] - mean) * rstd;
+        gw[n] = fmaf(g[n], xh[n], gw[n]);
+        gb[n] += g[n];
+        g[n] *= w[e];
+        s1 += g[n];
+        s2 = fmaf(g[n], xh[n], s2);
+      }
+    }
+    s1 = row_sum<TPR>(s1, red, turn) * inv_d;
+    s2 = row_sum<TPR>(s2, red, turn) * inv_d;
+    if (!on) continue;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * TPR + tr) * V;
+      if (c >= a.D) continue;
+      float o[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = rstd * (g[i * V + e] - s1 - xh[i * V + e] * s2);
+      st_vec<TO, V>(dx + row * a.D + c, o);
+    }
+  }
+  // the block's partial sums: its rows of threads are added in order
+  auto leave = [&](const float* v, float* out) {
+    if (!out) return;
+    float* p = out + (size_t)blockIdx.x * a.D;
+    if constexpr (RPB == 1) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + tr) * V;
+        if (c < a.D) st_vec<float, V>(p + c, v + i * V);
+      }
+    } else {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + tr) * V;
+        if (c < a.D) st_vec<float, V>(part + (size_t)rb * a.D + c, v + i * V);
+      }
+      __syncthreads();
+      for (int c = threadIdx.x; c < a.D; c += kThreads) {
+        float s = part[c];
+#pragma unroll
+        for (int r = 1; r < RPB; ++r) s += part[(size_t)r * a.D + c];
+        p[c] = s;
+      }
+    }
+  };
+  leave(gw, a.pw);
+  leave(gb, a.pb);
+}
+
+// Rows of any width: one block per row at a time, re-read from cache; the block's
+// weight gradients are kept in its partial rows in global memory.
+template <typename T, typename TO>
+__global__ void __launch_bounds__(kThreads) ln_bwd_wide_kernel(const LnBwdArgs a) {
+  __shared__ float red[2 * kThreads / 32];
+  int turn = 0;
+  const float inv_d = 1.f / a.D;
+  griddep_wait();
+  griddep_launch_dependents();
+  float* pw = a.pw ? a.pw + (size_t)blockIdx.x * a.D : nullptr;
+  float* pb = a.pb ? a.pb + (size_t)blockIdx.x * a.D : nullptr;
+  for (int c = threadIdx.x; c < a.D; c += kThreads) {  // a column stays with one thread
+    if (pw) pw[c] = 0.f;
+    if (pb) pb[c] = 0.f;
+  }
+  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    const T* dy = static_cast<const T*>(a.dy) + row * a.D;
+    TO* dx = static_cast<TO*>(a.dx) + row * a.D;
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float s1 = 0.f, s2 = 0.f;
+    for (int c = threadIdx.x; c < a.D; c += kThreads) {
+      const float g = static_cast<float>(dy[c]), xh = (static_cast<float>(x[c]) - mean) * rstd;
+      if (pw) pw[c] += g * xh;
+      if (pb) pb[c] += g;
+      const float aw = a.w ? g * a.w[c] : g;
+      s1 += aw;
+      s2 = fmaf(aw, xh, s2);
+    }
+    s1 = row_sum<kThreads>(s1, red, turn) * inv_d;
+    s2 = row_sum<kThreads>(s2, red, turn) * inv_d;
+    for (int c = threadIdx.x; c < a.D; c += kThreads) {
+      const float g = static_cast<float>(dy[c]), xh = (static_cast<float>(x[c]) - mean) * rstd;
+      const float v = rstd * ((a.w ? g * a.w[c] : g) - s1 - xh * s2);
+      st_vec<TO, 1>(dx + c, &v);
+    }
+  }
+}
+
+// out[c] = sum of the blocks' partial rows: 32 columns per block, eight groups of
+// rows whose sums are added in order.
+__global__ void __launch_bounds__(256) ln_bwd_join_kernel(const float* __restrict__ pw, const float* __restrict__ pb,
+                                                          float* dw, float* db, int blocks, int D) {
+  __shared__ float part[8][33];
+  griddep_wait();
+  griddep_launch_dependents();
+  const float* p = blockIdx.y ? pb : pw;
+  float* out = blockIdx.y ? db : dw;
+  if (!out) return;
+  const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (c < D)
+    for (int r = grp; r < blocks; r += 8) s += p[(size_t)r * D + c];
+  part[grp][lane] = s;
+  __syncthreads();
+  if (grp == 0 && c < D) {
+#pragma unroll
+    for (int g = 1; g < 8; ++g) s += part[g][lane];
+    out[c] = s;
+  }
+}
+
+// Blocks for `rows` rows of which a block takes `rpb` at a time.
+int ln_blocks(long long rows, int rpb, int cap) {
+  const long long n = (rows + rpb - 1) / rpb;
+  return (int)(n < 1 ? 1 : (n < cap ? n : cap));
+}
+constexpr int kFwdBlocks = 148 * 8;
+
+// Picks <V, NV, TPR> for D: 16-byte vectors where `vec` allows them, a warp per
+// row up to 1024 values (32 per lane), 128 threads up to 4096, 256 up to 8192.
+template <typename T, typename F>
+cudaError_t ln_pick(int D, bool vec, F&& f) {
+  constexpr int V = 16 / sizeof(T);
+  auto go = [&](auto v) {
+    constexpr int W = decltype(v)::value;
+    using std::integral_constant;
+    if (D <= 256) return f(integral_constant<int, W>{}, integral_constant<int, 8 / W>{}, integral_constant<int, 32>{});
+    if (D <= 512) return f(integral_constant<int, W>{}, integral_constant<int, 16 / W>{}, integral_constant<int, 32>{});
+    if (D <= 1024) return f(integral_constant<int, W>{}, integral_constant<int, 32 / W>{}, integral_constant<int, 32>{});
+    if (D <= 2048) return f(integral_constant<int, W>{}, integral_constant<int, 16 / W>{}, integral_constant<int, 128>{});
+    if (D <= 4096) return f(integral_constant<int, W>{}, integral_constant<int, 32 / W>{}, integral_constant<int, 128>{});
+    return f(integral_constant<int, W>{}, integral_constant<int, 32 / W>{}, integral_constant<int, 256>{});
+  };
+  return vec ? go(std::integral_constant<int, V>{}) : go(std::integral_constant<int, 1>{});
+}
+
+template <typename T, typename TO>
+cudaError_t ln_fwd_launch(const LnArgs& a, bool vec, cudaStream_t s) {
+  if (a.D > 8192) return launch_pdl(ln_fwd_wide_kernel<T, TO>, dim3(ln_blocks(a.rows, 1, kFwdBlocks)), dim3(kThreads), 0, s, a);
+  return ln_pick<T>(a.D, vec, [&](auto v, auto nv, auto tpr) {
+    constexpr int TPR = decltype(tpr)::value;
+    return launch_pdl(ln_fwd_kernel<T, TO, decltype(v)::value, decltype(nv)::value, TPR>,
+                      dim3(ln_blocks(a.rows, kThreads / TPR, kFwdBlocks)), dim3(kThreads), 0, s, a);
+  });
+}
+
+// Launches the backward; *blocks is the number of partial rows it leaves.
+template <typename T, typename TO>
+cudaError_t ln_bwd_launch(const LnBwdArgs& a, bool vec, cudaStream_t s, int* blocks) {
+  if (a.D > 8192) {
+    *blocks = ln_blocks(a.rows, 1, kMaxBlocks);
+    return launch_pdl(ln_bwd_wide_kernel<T, TO>, dim3(*blocks), dim3(kThreads), 0, s, a);
+  }
+  return ln_pick<T>(a.D, vec, [&](auto v, auto nv, auto tpr) {
+    constexpr int TPR = decltype(tpr)::value, RPB = kThreads / TPR;
+    const size_t smem = RPB > 1 ? (size_t)RPB * a.D * 4 : 0;  // at most 8 * 1024 or 2 * 4096 floats
+    *blocks = ln_blocks(a.rows, RPB, kMaxBlocks);
+    auto k = ln_bwd_kernel<T, TO, decltype(v)::value, decltype(nv)::value, TPR>;
+    return launch_pdl(k, dim3(*blocks), dim3(kThreads), smem, s, a);
+  });
+}
+
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+dig_status ln_fail(dig_status s, const char* msg) {
+  set_last_error(msg);
+  return s;
+}
+
+dig_status ln_check(long long rows, int D, long long x_stride, int dtype, int out_dtype) {
+  if (rows < 0 || D <= 0) return ln_fail(DIG_ERR_INVALID_ARGUMENT, "layer norm: rows must be >= 0 and D >= 1");
+  if (x_stride < D) return ln_fail(DIG_ERR_INVALID_ARGUMENT, "layer norm: x_stride must be at least D");
+  if ((dtype != DIG_F32 && dtype != DIG_BF16) || (out_dtype != DIG_F32 && out_dtype != DIG_BF16))
+    return ln_fail(DIG_ERR_INVALID_ARGUMENT, "layer norm: dtype / out_dtype not DIG_F32 or DIG_BF16");
+  if (rows >= (1ll << 40) / x_stride) return ln_fail(DIG_ERR_INVALID_ARGUMENT, "layer norm: tensor too large");
+  return DIG_OK;
+}
+
+// Whether every row of the dense tensors and of x starts at a 16-byte boundary.
+bool ln_vec(int D, long long x_stride, int dtype) {
+  const int v = dtype == DIG_BF16 ? 8 : 4;
+  return D % v == 0 && x_stride % v == 0;
+}
+
+}  // namespace
+}  // namespace dig
+
+using namespace dig;
+
+extern "C" {
+
+size_t dig_layer_norm_workspace_bytes(long long rows, int D) {
+  if (rows < 0 || D <= 0) return 0;
+  return (size_t)2 * (rows < kMaxBlocks ? (rows < 1 ? 1 : rows) : kMaxBlocks) * D * 4;
+}
+
+dig_status dig_layer_norm_fwd(const void* x, long long x_stride, const float* weight, const float* bias, float eps,
+                              void* y, float* mean, float* rstd, long long rows, int D, int dtype, int out_dtype,
+                              void* stream) {
+  const dig_status st = ln_check(rows, D, x_stride, dtype, out_dtype);
+  if (st != DIG_OK) return st;
+  if (!(eps >= 0.f)) return ln_fail(DIG_ERR_INVALID_ARGUMENT, "layer norm: eps must be >= 0");
+  if (rows == 0) return DIG_OK;
+  if (!x || !y) return ln_fail(DIG_ERR_INVALID_ARGUMENT, "layer norm: x and y must be non-NULL");
+  if (!al16(x) || !al16(y) || !al16(weight) || !al16(bias) || !al16(mean) || !al16(rstd))
+    return ln_fail(DIG_ERR_MISALIGNED, "layer norm: a tensor pointer is not 16-byte aligned");
+  const LnArgs a{x, x_stride, weight, bias, eps, y, mean, rstd, rows, D};
+  const bool vec = ln_vec(D, x_stride, dtype);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == DIG_BF16
+                            ? (out_dtype == DIG_BF16 ? ln_fwd_launch<__nv_bfloat16, __nv_bfloat16>(a, vec, s)
+                                                     : ln_fwd_launch<__nv_bfloat16, float>(a, vec, s))
+                            : (out_dtype == DIG_BF16 ? ln_fwd_launch<float, __nv_bfloat16>(a, vec, s)
+                                                     : ln_fwd_launch<float, float>(a, vec, s));
+  return e == cudaSuccess ? DIG_OK : ln_fail(DIG_ERR_CUDA, cudaGetErrorString(e));
+}
+
+dig_status dig_layer_norm_bwd(const void* x, long long x_stride, const float* weight, const float* mean,
+                              const float* rstd, const void* dy, void* dx, float* dweight, float* dbias, long long rows,
+                              int D, int dtype, int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  const dig_status st = ln_check(rows, D, x_stride, dtype, out_dtype);
+  if (st != DIG_OK) return st;
+  if (rows > 0 && (!x || !mean || !rstd || !dy || !dx))
+    return ln_fail(DIG_ERR_INVALID_ARGUMENT, "layer norm backward: x, mean, rstd, dy and dx must be non-NULL");
+  if (!al16(x) || !al16(weight) || !al16(mean) || !al16(rstd) || !al16(dy) || !al16(dx) || !al16(dweight) ||
+      !al16(dbias) || !al16(workspace))
+    return ln_fail(DIG_ERR_MISALIGNED, "layer norm backward: a tensor pointer is not 16-byte aligned");
+  const bool par = dweight || dbias;
+  if (par && !workspace) return ln_fail(DIG_ERR_INVALID_ARGUMENT, "layer norm backward: dweight and dbias need a workspace");
+  if (par && workspace_bytes < dig_layer_norm_workspace_bytes(rows, D))
+    return ln_fail(DIG_ERR_WORKSPACE_TOO_SMALL, "layer norm backward: workspace too small");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float* part = static_cast<float*>(workspace);
+  // the partial rows: [blocks][D] of dweight, then of dbias
+  const size_t half = dig_layer_norm_workspace_bytes(rows, D) / 8;
+  LnBwdArgs a{x, x_stride, weight, mean, rstd, dy, dx, dweight ? part : nullptr, dbias ? part + half : nullptr, rows, D};
+  int blocks = 0;
+  cudaError_t e = cudaSuccess;
+  if (rows > 0) {
+    const bool vec = ln_vec(D, x_stride, dtype);
+    e = dtype == DIG_BF16 ? (out_dtype == DIG_BF16 ? ln_bwd_launch<__nv_bfloat16, __nv_bfloat16>(a, vec, s, &blocks)
+                                                   : ln_bwd_launch<__nv_bfloat16, float>(a, vec, s, &blocks))
+                          : (out_dtype == DIG_BF16 ? ln_bwd_launch<float, __nv_bfloat16>(a, vec, s, &blocks)
+                                                   : ln_bwd_launch<float, float>(a, vec, s, &blocks));
+  }
+  if (e == cudaSuccess && par)
+    e = launch_pdl(ln_bwd_join_kernel, dim3((D + 31) / 32, 2), dim3(256), 0, s, a.pw, a.pb, dweight, dbias, blocks, D);
+  return e == cudaSuccess ? DIG_OK : ln_fail(DIG_ERR_CUDA, cudaGetErrorString(e));
+}
+
+}  // extern "C"

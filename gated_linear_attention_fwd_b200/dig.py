@@ -83,6 +83,24 @@ lib.dig_block_gated_add.restype = _i
 lib.dig_block_gated_add.argtypes = [_vp, _vp, ctypes.c_longlong, _vp, _i, ctypes.c_longlong, _i, _vp]
 lib.dig_block_activation.restype = _i
 lib.dig_block_activation.argtypes = [_vp, ctypes.c_longlong, _i, _vp]
+_ll = ctypes.c_longlong
+lib.dig_decay_attn_fwd.restype = _i
+lib.dig_decay_attn_fwd.argtypes = [_vp, _vp, _vp, _ll, _ll, _ll, _vp, _f, _vp, _vp, _vp, _vp, _i, _vp,
+                                   _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _sz, _vp]
+lib.dig_decay_attn_bwd.restype = _i
+lib.dig_decay_attn_bwd.argtypes = [_vp, _vp, _vp, _ll, _ll, _ll, _vp, _f, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                   _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _sz, _vp]
+lib.dig_decay_attn_workspace_bytes.restype = _sz
+lib.dig_decay_attn_workspace_bytes.argtypes = [_i, _i, _i, _i, _i, _i, _i, _i]
+lib.dig_decay_attn_step.restype = _i
+lib.dig_decay_attn_step.argtypes = [_vp, _vp, _vp, _ll, _ll, _ll, _vp, _f, _vp, _vp, _i, _vp,
+                                    _i, _i, _i, _i, _i, _i, _vp, _vp]
+lib.dig_layer_norm_fwd.restype = _i
+lib.dig_layer_norm_fwd.argtypes = [_vp, _ll, _vp, _vp, _f, _vp, _vp, _vp, _ll, _i, _i, _i, _vp]
+lib.dig_layer_norm_bwd.restype = _i
+lib.dig_layer_norm_bwd.argtypes = [_vp, _ll, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _ll, _i, _i, _i, _vp, _sz, _vp]
+lib.dig_layer_norm_workspace_bytes.restype = _sz
+lib.dig_layer_norm_workspace_bytes.argtypes = [_ll, _i]
 lib.dig_read_status.restype = _i
 lib.dig_read_status.argtypes = [_vp, _vp]
 lib.dig_status_string.restype = ctypes.c_char_p
@@ -305,6 +323,225 @@ def dig_block_activation(x, kind, stream=None):
     """In place on bf16 x: kind 0 SiLU, kind 1 GELU (tanh form)."""
     st = lib.dig_block_activation(_ptr(x), x.numel(), int(kind), _stream(stream))
     _check(st, "dig_block_activation")
+
+
+# ------------------------------------------------------------------ head-decay attention, layer norm
+_CODES = {torch.float32: DIG_F32, torch.bfloat16: DIG_BF16}
+
+
+def _typed(t):
+    c = _CODES.get(t.dtype)
+    if c is None:
+        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % t.dtype)
+    return c
+
+
+def _dense(t, name, shape, dtype, dev):
+    """Address of a contiguous tensor of exactly this shape, dtype and device (None: NULL)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s, got %s %s on %s%s" % (
+            name, dtype, tuple(shape), dev, t.dtype, tuple(t.shape), t.device, "" if t.is_contiguous() else ", strided"))
+    return t.data_ptr()
+
+
+def _tokens(t, name, H, d):
+    """Rows of a [..., H, d] tensor whose H * d values are dense, and the elements between rows."""
+    if t.shape[-2:] != (H, d):
+        raise ValueError("%s must be [..., %d, %d], got %s" % (name, H, d, tuple(t.shape)))
+    st = t.stride()
+    if (d > 1 and st[-1] != 1) or (H > 1 and st[-2] != d):
+        raise ValueError("%s: the %d x %d values of a token must be dense" % (name, H, d))
+    return _row_stride(t, name, 2, H * d)
+
+
+def _row_stride(t, name, inner, size):
+    """Elements between the rows of t (all dimensions but the last `inner`), which must be one apart in every dimension."""
+    shape, st = t.shape[:-inner], t.stride()
+    step, rows = None, 1
+    if t.numel() == 0:
+        return size
+    for n, s in zip(reversed(shape), reversed(st[:len(shape)])):
+        if n == 1:
+            continue
+        if step is None:
+            step = s
+        elif s != step * rows:
+            raise ValueError("%s: its rows must be one stride apart" % name)
+        rows *= n
+    return size if step is None else step
+
+
+class _On:
+    """Makes a tensor's device current where it is not (launches go to the current device)."""
+    __slots__ = ("device", "guard")
+
+    def __init__(self, t):
+        if not t.is_cuda:
+            raise ValueError("tensors must be on a CUDA device")
+        self.device, self.guard = t.device, None
+
+    def __enter__(self):
+        if self.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
+
+
+def _raw_stream(stream, device):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def decay_attn_workspace_bytes(B, H, L, d_k, d_v, dtype=torch.bfloat16, packed=False, backward=False) -> int:
+    return int(lib.dig_decay_attn_workspace_bytes(B, H, L, d_k, d_v, _code(dtype), int(packed), int(backward)))
+
+
+def new_decay_attn_workspace(B, H, L, d_k, d_v, dtype=torch.bfloat16, packed=False, backward=False,
+                             device="cuda") -> torch.Tensor:
+    """A zero-filled workspace (uint8) for dig_decay_attn_fwd / dig_decay_attn_bwd; packed: B sequences in L rows."""
+    n = decay_attn_workspace_bytes(B, H, L, d_k, d_v, dtype, packed, backward)
+    if n == 0:
+        raise ValueError("unsupported shape for the head-decay attention")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _decay_shape(q, k, v, o, cu_seqlens, grid_h, grid_w):
+    """(B, H, L, d_k, d_v, grid_h, grid_w, row strides) of a call's q [B, L, H, d_k] (packed: [rows, H, d_k]), k, v."""
+    H, dk = q.shape[-2:]
+    dv = v.shape[-1]
+    lead = q.shape[:-2]
+    if k.shape != q.shape or v.shape[:-1] != q.shape[:-1]:
+        raise ValueError("q, k [..., H, d_k] and v [..., H, d_v] must agree: got %s, %s, %s" % (
+            tuple(q.shape), tuple(k.shape), tuple(v.shape)))
+    if not q.dtype == k.dtype == v.dtype or not q.device == k.device == v.device:
+        raise ValueError("q, k and v must have one dtype and device")
+    if cu_seqlens is not None:
+        if len(lead) != 1 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("packed sequences: q, k, v [rows, H, d] and cu_seqlens [B + 1]")
+        B, L = cu_seqlens.numel() - 1, lead[0]
+        grid_h, grid_w = 1, L
+    else:
+        if len(lead) != 2:
+            raise ValueError("q, k, v must be [B, L, H, d]")
+        B, L = lead
+        if grid_h is None and grid_w is None:
+            grid_h, grid_w = 1, L
+    return B, H, L, dk, dv, grid_h, grid_w, _tokens(q, "q", H, dk), _tokens(k, "k", H, dk), _tokens(v, "v", H, dv)
+
+
+def dig_decay_attn_fwd(q, k, v, log_decay, o, workspace, grid_h=None, grid_w=None, scan_mode=0, cu_seqlens=None,
+                       scale=1.0, S0=None, S_final=None, slots=None, stream=None):
+    """Linear attention with one decay per head (see include/dig.h): q, k [B,L,H,dk], v [B,L,H,dv] (token slices of one
+    projection may be passed), or packed [rows,H,d] with cu_seqlens [B+1] int32; log_decay [H] fp32; o like v, dense;
+    S0, S_final [B,H,dk,dv] fp32 or, with slots [B] int32, pools [n,H,dk,dv].  Without a grid the L tokens are a line."""
+    B, H, L, dk, dv, grid_h, grid_w, qs, ks, vs = _decay_shape(q, k, v, o, cu_seqlens, grid_h, grid_w)
+    dev = q.device
+    n = B
+    if slots is not None:
+        pool = S0 if S0 is not None else S_final
+        n = pool.shape[0] if pool is not None else 0
+    state = (n, H, dk, dv)
+    f32 = torch.float32
+    with _On(q):
+        st = lib.dig_decay_attn_fwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _dense(log_decay, "log_decay", (H,), f32, dev),
+            float(scale), _dense(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev), _dense(S0, "S0", state, f32, dev),
+            _dense(S_final, "S_final", state, f32, dev), _dense(slots, "slots", (B,), torch.int32, dev), n,
+            _dense(o, "o", v.shape, o.dtype, dev), B, H, L, dk, dv, grid_h, grid_w, scan_mode, _typed(q), _typed(o),
+            _dense(workspace, "workspace", workspace.shape, torch.uint8, dev), workspace.numel(), _raw_stream(stream, dev))
+    _check(st, "dig_decay_attn_fwd")
+
+
+def dig_decay_attn_bwd(q, k, v, log_decay, dO, dq, dk, dv, workspace, grid_h=None, grid_w=None, scan_mode=0,
+                       cu_seqlens=None, scale=1.0, S0=None, dS_final=None, dS0=None, stream=None):
+    """Gradients for dig_decay_attn_fwd (see include/dig.h): dO like v, dq, dk like q and dv like v, all dense;
+    S0, dS_final, dS0 [B,H,dk,dv] fp32."""
+    B, H, L, d_k, d_v, grid_h, grid_w, qs, ks, vs = _decay_shape(q, k, v, dO, cu_seqlens, grid_h, grid_w)
+    dev = q.device
+    state = (B, H, d_k, d_v)
+    f32 = torch.float32
+    with _On(q):
+        st = lib.dig_decay_attn_bwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _dense(log_decay, "log_decay", (H,), f32, dev),
+            float(scale), _dense(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev), _dense(S0, "S0", state, f32, dev),
+            _dense(dO, "dO", v.shape, q.dtype, dev), _dense(dS_final, "dS_final", state, f32, dev),
+            _dense(dq, "dq", q.shape, dq.dtype, dev), _dense(dk, "dk", q.shape, dq.dtype, dev),
+            _dense(dv, "dv", v.shape, dq.dtype, dev), _dense(dS0, "dS0", state, f32, dev),
+            B, H, L, d_k, d_v, grid_h, grid_w, scan_mode, _typed(q), _typed(dq),
+            _dense(workspace, "workspace", workspace.shape, torch.uint8, dev), workspace.numel(), _raw_stream(stream, dev))
+    _check(st, "dig_decay_attn_bwd")
+
+
+def dig_decay_attn_step(q, k, v, log_decay, S, o, slots=None, scale=1.0, device_status=None, stream=None):
+    """One token for each of B sequences: q, k [B,H,dk], v [B,H,dv]; S [n,H,dk,dv] fp32, updated in place (row b uses
+    state slots[b], or b); o [B,H,dv].  device_status: optional zeroed int32 [1] (see include/dig.h)."""
+    B, H, dk = q.shape
+    dv = v.shape[2]
+    dev = q.device
+    if k.shape != q.shape or v.shape[:2] != q.shape[:2] or not q.dtype == k.dtype == v.dtype or \
+            not dev == k.device == v.device:
+        raise ValueError("q, k [B, H, d_k] and v [B, H, d_v] must agree in shape, dtype and device")
+    n = S.shape[0]
+    with _On(q):
+        st = lib.dig_decay_attn_step(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), _tokens(q, "q", H, dk), _tokens(k, "k", H, dk),
+            _tokens(v, "v", H, dv), _dense(log_decay, "log_decay", (H,), torch.float32, dev), scale,
+            _dense(S, "S", (n, H, dk, dv), torch.float32, dev), _dense(slots, "slots", (B,), torch.int32, dev), n,
+            _dense(o, "o", v.shape, o.dtype, dev), B, H, dk, dv, _typed(q), _typed(o),
+            _dense(device_status, "device_status", (1,), torch.int32, dev), _raw_stream(stream, dev))
+    if st != DIG_OK:
+        _check(st, "dig_decay_attn_step")
+
+
+def dig_layer_norm_fwd(x, y, weight=None, bias=None, eps=1e-5, mean=None, rstd=None, stream=None):
+    """y = (x - mean) * rstd * weight + bias over the last dimension; x [..., D] (rows one stride apart), y dense;
+    weight, bias [D] fp32; mean, rstd [rows] fp32 outputs."""
+    D = x.shape[-1]
+    dev = x.device
+    if x.dim() < 1 or D == 0 or (D > 1 and x.stride(-1) != 1):
+        raise ValueError("x must be [..., D] with dense rows")
+    rows = x.numel() // D
+    f32 = torch.float32
+    with _On(x):
+        st = lib.dig_layer_norm_fwd(
+            x.data_ptr(), _row_stride(x, "x", 1, D), _dense(weight, "weight", (D,), f32, dev),
+            _dense(bias, "bias", (D,), f32, dev), eps, _dense(y, "y", x.shape, y.dtype, dev),
+            _dense(mean, "mean", (rows,), f32, dev), _dense(rstd, "rstd", (rows,), f32, dev), rows, D, _typed(x),
+            _typed(y), _raw_stream(stream, dev))
+    if st != DIG_OK:
+        _check(st, "dig_layer_norm_fwd")
+
+
+def new_layer_norm_workspace(rows, D, device="cuda") -> torch.Tensor:
+    """A workspace (uint8) for dig_layer_norm_bwd with dw or db."""
+    return torch.empty(int(lib.dig_layer_norm_workspace_bytes(rows, D)), dtype=torch.uint8, device=device)
+
+
+def dig_layer_norm_bwd(x, dy, mean, rstd, dx, weight=None, dw=None, db=None, workspace=None, stream=None):
+    """Gradients for dig_layer_norm_fwd: x as there, dy, dx dense and like x; mean, rstd [rows] of the forward; dw, db
+    [D] fp32 (either needs the workspace)."""
+    D = x.shape[-1]
+    dev = x.device
+    if x.dim() < 1 or D == 0 or (D > 1 and x.stride(-1) != 1):
+        raise ValueError("x must be [..., D] with dense rows")
+    rows = x.numel() // D
+    f32 = torch.float32
+    with _On(x):
+        st = lib.dig_layer_norm_bwd(
+            x.data_ptr(), _row_stride(x, "x", 1, D), _dense(weight, "weight", (D,), f32, dev),
+            _dense(mean, "mean", (rows,), f32, dev), _dense(rstd, "rstd", (rows,), f32, dev),
+            _dense(dy, "dy", x.shape, x.dtype, dev), _dense(dx, "dx", x.shape, dx.dtype, dev),
+            _dense(dw, "dw", (D,), f32, dev), _dense(db, "db", (D,), f32, dev), rows, D, _typed(x), _typed(dx),
+            None if workspace is None else _dense(workspace, "workspace", workspace.shape, torch.uint8, dev),
+            0 if workspace is None else workspace.numel(), _raw_stream(stream, dev))
+    if st != DIG_OK:
+        _check(st, "dig_layer_norm_bwd")
 
 
 def dig_read_status(workspace, stream=None) -> int:

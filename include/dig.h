@@ -327,6 +327,98 @@ dig_status dig_block_gated_add(void *x, const float *gate, long long mod_stride,
                                long long rows_per_batch, int D, void *stream);
 dig_status dig_block_activation(void *x, long long n, int kind, void *stream);
 
+/* Linear attention with one decay per head: the form of GLA (slide eq. (6)-(8))
+ * whose gate is a constant of the head, alpha_t = lambda_h = exp(log_decay[h]):
+ *   S_t = lambda S_{t-1} + k_t^T v_t,   o_t = scale * q_t S_t
+ * over B sequences in scan order, started from S0.
+ *   q, k   [rows, H, d_k] dtype     the H * d_k values of a token are dense; tokens are
+ *   v      [rows, H, d_v] dtype     q_stride / k_stride / v_stride elements apart (slices
+ *                                   of one fused projection may be passed)
+ *   log_decay [H] fp32, <= 0        -INFINITY (lambda = 0) is allowed
+ *   o      [rows, H, d_v] out_dtype dense
+ *   cu_seqlens  NULL: B sequences of L = grid_h * grid_w tokens each, rows = B * L, scanned
+ *               in scan_mode (as dig_gla_fwd).  Else [B + 1] int32, non-decreasing, within
+ *               0 .. L: sequence b is the rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 of
+ *               L rows, scanned in ROW_FWD or ROW_REV order (grid_h, grid_w are not read);
+ *               a sequence may be empty, and rows of no sequence are left as they were
+ *   S0     [B, H, d_k, d_v] fp32    initial states; NULL: zero
+ *   S_final [B, H, d_k, d_v] fp32   states after the last scan position; NULL: not wanted;
+ *                                   may be S0 itself (continued in place)
+ *   slots  [B] int32 or NULL        S0 and S_final are pools [n_slots, H, d_k, d_v] and
+ *               sequence b uses state slots[b]; a negative one starts from zero and
+ *               leaves no state.  Slots must differ (negative ones aside).
+ * d_k and d_v are multiples of 4 up to 128, strides multiples of 4 elements; else
+ * DIG_ERR_UNSUPPORTED.  q, k and v are aligned to four elements, the rest to 16 bytes.  Values have to be finite: a NaN or infinity may reach other
+ * tokens of its own sequence (never another sequence's).  Offsets and slots live on the
+ * device: a bad offset (clamped to its range), a slot of n_slots or more or one that an
+ * earlier sequence has (then taken as negative) sets DIG_ERR_INVALID_ARGUMENT in the
+ * workspace's status word.  The workspace (dig_decay_attn_workspace_bytes, zero-filled
+ * before the first use) is scratch of one call at a time.  Results do not depend on
+ * what shares the call and are the same from run to run. */
+dig_status dig_decay_attn_fwd(const void *q, const void *k, const void *v, long long q_stride,
+                              long long k_stride, long long v_stride, const float *log_decay, float scale,
+                              const int *cu_seqlens, const float *S0, float *S_final, const int *slots,
+                              int n_slots, void *o, int B, int H, int L, int d_k, int d_v, int grid_h,
+                              int grid_w, int scan_mode, int dtype, int out_dtype, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* Gradients for dig_decay_attn_fwd of sum(o * dO) + sum(S_final * dS_final) (the
+ * decays are constants of the model and get none).  Arguments as the forward's, plus:
+ *   dO         [rows, H, d_v] dtype, dense
+ *   dS_final   [B, H, d_k, d_v] fp32 or NULL (zero)
+ *   dq, dk     [rows, H, d_k] out_dtype;  dv [rows, H, d_v] out_dtype; dense; rows of no
+ *              sequence are left as they were
+ *   dS0        [B, H, d_k, d_v] fp32 or NULL: the gradient of S0
+ * Nothing of the forward is kept: the states are computed again. */
+dig_status dig_decay_attn_bwd(const void *q, const void *k, const void *v, long long q_stride,
+                              long long k_stride, long long v_stride, const float *log_decay, float scale,
+                              const int *cu_seqlens, const float *S0, const void *dO, const float *dS_final,
+                              void *dq, void *dk, void *dv, float *dS0, int B, int H, int L, int d_k, int d_v,
+                              int grid_h, int grid_w, int scan_mode, int dtype, int out_dtype, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace dig_decay_attn_fwd (pass = 0) or dig_decay_attn_bwd (pass = 1)
+ * needs; packed: whether cu_seqlens is given (L = its rows).  0 for invalid shapes. */
+size_t dig_decay_attn_workspace_bytes(int B, int H, int L, int d_k, int d_v, int dtype, int packed, int pass);
+
+/* One token for each of B sequences (the recurrent form, for decoding): per row b
+ *   S = lambda S + k_b^T v_b (in place),   o_b = scale * q_b S
+ *   q, k [B, H, d_k], v [B, H, d_v] dtype, rows q_stride / k_stride / v_stride apart
+ *   S    [n_slots, H, d_k, d_v] fp32; slots [B] int32, or NULL: row b uses state b
+ *        (n_slots >= B).  A negative slot marks a padding row: its o is left as it was.
+ *        Slots must differ: a row whose slot an earlier row has, or whose slot is
+ *        n_slots or more, is left out like padding and DIG_ERR_INVALID_ARGUMENT goes to
+ *        device_status.
+ *   o    [B, H, d_v] out_dtype, dense
+ *   device_status (optional device word, set to zero by the caller beforehand)
+ * d_k and d_v multiples of 4 up to 256, strides multiples of 4; q, k and v aligned to
+ * four elements, S and o to 16 bytes. */
+dig_status dig_decay_attn_step(const void *q, const void *k, const void *v, long long q_stride,
+                               long long k_stride, long long v_stride, const float *log_decay, float scale,
+                               float *S, const int *slots, int n_slots, void *o, int B, int H, int d_k, int d_v,
+                               int dtype, int out_dtype, unsigned int *device_status, void *stream);
+
+/* Layer norm over rows of D values (slide eq. (10) writes LN):
+ *   y = (x - mean) * rstd * weight + bias,   rstd = 1 / sqrt(var + eps), var over D
+ *   x  [rows, D] dtype, rows x_stride elements apart (>= D);  y [rows, D] out_dtype, dense
+ *   weight, bias [D] fp32 or NULL (ones, zeros);  mean, rstd [rows] fp32 or NULL
+ * Any D >= 1 and any stride; 16-byte accesses where D and the stride allow them. */
+dig_status dig_layer_norm_fwd(const void *x, long long x_stride, const float *weight, const float *bias,
+                              float eps, void *y, float *mean, float *rstd, long long rows, int D, int dtype,
+                              int out_dtype, void *stream);
+
+/* Gradients for dig_layer_norm_fwd of sum(y * dy):
+ *   x [rows, D] dtype (x_stride as above), mean, rstd [rows] fp32 of the forward
+ *   dy [rows, D] dtype, dense;  dx [rows, D] out_dtype, dense
+ *   dweight, dbias [D] fp32 or NULL: sums over the rows (overwritten), added in a fixed
+ *   order, so the same from run to run; with either the workspace
+ *   (dig_layer_norm_workspace_bytes; any contents) is needed. */
+dig_status dig_layer_norm_bwd(const void *x, long long x_stride, const float *weight, const float *mean,
+                              const float *rstd, const void *dy, void *dx, float *dweight, float *dbias,
+                              long long rows, int D, int dtype, int out_dtype, void *workspace,
+                              size_t workspace_bytes, void *stream);
+size_t dig_layer_norm_workspace_bytes(long long rows, int D);
+
 /* Synchronises `stream`, returns the device status word kept in `workspace`
  * (DIG_OK, DIG_ERR_DEVICE_TIMEOUT or DIG_ERR_GATE_RANGE) and clears it. */
 dig_status dig_read_status(void *workspace, void *stream);
