@@ -6,6 +6,7 @@
 
 #include "decay_attn.h"
 #include "sm100.cuh"
+#include "tmap.h"
 
 namespace dig {
 
@@ -51,7 +52,7 @@ Cut cut_of(int B, int H, int L, int dk, int dv, int chunk, int per_sm, bool pack
       const int ns = L > 0 ? (L + seg - 1) / seg : 1;
       const long long units = (long long)B * H * nprob * ns;
       const double waves = (double)((units + slots - 1) / slots);
-      const double cost = waves * (seg / chunk) * (ns > 1 ? 1.5 : 1.0) + (ns > 1 ? 1.0 + 0.15 * (ns - 1) : 0.0);
+      const double cost = waves * (seg / chunk + 1) * (ns > 1 ? 1.5 : 1.0) + (ns > 1 ? 1.0 + 0.15 * (ns - 1) : 0.0);
       if (n == 1 || cost < best) {
         best = cost;
         r.seg = seg;
@@ -83,9 +84,13 @@ bool size_ok(int B, int H, int L, int d_k, int d_v, bool packed) {
          H <= 65535;
 }
 
-Cut cut_for(int B, int H, int L, int dk, int dv, int dtype, bool packed, int nprob) {
-  (void)dtype;
-  return cut_of(B, H, L, dk, dv, 32, dk > 64 || dv > 64 ? 1 : 3, packed, nprob);
+// bf16 in and out runs on the tensor core (chunks of 128 tokens), the rest on the FP32 pipes (chunks of 32).
+bool on_tc(int dtype, int out_dtype) { return dtype == DIG_BF16 && out_dtype == DIG_BF16; }
+
+Cut cut_for(int B, int H, int L, int dk, int dv, bool tc, bool packed, int nprob) {
+  const bool small = dk <= 64 && dv <= 64;
+  return tc ? cut_of(B, H, L, dk, dv, 128, small ? 2 : 1, packed, nprob)
+            : cut_of(B, H, L, dk, dv, 32, small ? 3 : 1, packed, nprob);
 }
 
 // The checks that the forward and the backward share.
@@ -117,6 +122,27 @@ dig_status check(const void* q, const void* k, const void* v, long long qs, long
   return DIG_OK;
 }
 
+// Maps of the call's tensors for the TMA, where alignment and the scan allow them: whole rows of tokens in the row
+// orders (and where the grid is one row or column), runs of 16 tokens of a column in the column orders.
+struct MapSource {
+  const void* base;
+  int d;
+  long long stride;
+};
+void encode_maps(DecayArgs& a, const MapSource* t, int n, int mode) {
+  a.fetch = kFetchTokens;
+  const bool rows = a.cu || mode < 2 || a.Hg == 1 || a.Wg == 1;
+  if (a.L == 0 || (!rows && a.Hg % kColRun) || !tmap_available()) return;
+  for (int i = 0; i < n; ++i) {
+    if (!al16(t[i].base) || t[i].d % 8 || t[i].stride % 8) return;
+    const uint64_t st = (uint64_t)t[i].stride, L = (uint64_t)a.L;
+    const uint64_t len[2][3] = {{L, a.cu ? 1u : (uint64_t)a.B, 1}, {(uint64_t)a.Hg, (uint64_t)a.Wg, (uint64_t)a.B}};
+    const uint64_t stride[2][3] = {{st, L * st, L * st}, {st * (uint64_t)a.Wg, st, L * st}};
+    if (!tmap_heads(&a.map[i], t[i].base, t[i].d, a.H, len[!rows], stride[!rows], rows ? 128 : kColRun)) return;
+  }
+  a.fetch = rows ? kFetchRows : kFetchCols;
+}
+
 dig_status launch(DecayArgs& a, int nprob, const Cut& c, void* ws, int dtype, int out_dtype, cudaStream_t s) {
   a.seg = c.seg;
   a.nps = c.nps;
@@ -124,7 +150,8 @@ dig_status launch(DecayArgs& a, int nprob, const Cut& c, void* ws, int dtype, in
   a.segst_problem = (long long)c.total * a.H * c.D * c.D;
   a.status = &static_cast<WsHeader*>(ws)->status;
   a.spin_ns = spin_limit_ns();
-  const cudaError_t e = launch_decay_f32(a, nprob, c.total, c.multi, c.D, dtype, out_dtype, s);
+  const cudaError_t e = on_tc(dtype, out_dtype) ? launch_decay_tc(a, nprob, c.total, c.multi, c.D, s)
+                                                : launch_decay_f32(a, nprob, c.total, c.multi, c.D, dtype, out_dtype, s);
   return e == cudaSuccess ? DIG_OK : attn_fail(DIG_ERR_CUDA, cudaGetErrorString(e));
 }
 
@@ -139,7 +166,12 @@ size_t dig_decay_attn_workspace_bytes(int B, int H, int L, int d_k, int d_v, int
   if (B < 0 || H <= 0 || L < 0 || d_k <= 0 || d_v <= 0 || d_k > 128 || d_v > 128 || d_k % 4 || d_v % 4 ||
       (pass != 0 && pass != 1) || (dtype != DIG_F32 && dtype != DIG_BF16) || !size_ok(B, H, L, d_k, d_v, packed != 0))
     return 0;
-  return sizeof(WsHeader) + cut_for(B, H, L, d_k, d_v, dtype, packed != 0, pass ? 3 : 1).states * sizeof(float);
+  size_t n = cut_for(B, H, L, d_k, d_v, false, packed != 0, pass ? 3 : 1).states;
+  if (dtype == DIG_BF16) {  // either output type
+    const size_t m = cut_for(B, H, L, d_k, d_v, true, packed != 0, pass ? 3 : 1).states;
+    n = m > n ? m : n;
+  }
+  return sizeof(WsHeader) + n * sizeof(float);
 }
 
 dig_status dig_decay_attn_fwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
@@ -159,8 +191,12 @@ dig_status dig_decay_attn_fwd(const void* q, const void* k, const void* v, long 
   a.slots = (S0 || S_final) ? slots : nullptr;
   a.n_slots = n_slots;
   a.B = B, a.H = H, a.L = L, a.Hg = grid_h, a.Wg = grid_w;
-  a.p[0] = DecayProblem{q, k, v, o, q_stride, k_stride, v_stride, S0, S_final, d_k, d_v, 0, 0, scan_mode, scale, 1.f, scale};
-  const Cut c = cut_for(B, H, L, d_k, d_v, dtype, cu_seqlens != nullptr, 1);
+  a.p[0] = DecayProblem{q, k, v, o, q_stride, k_stride, v_stride, S0, S_final, d_k, d_v, 0, 0, scan_mode, scale, 1.f, scale, 0, 1, 2};
+  if (on_tc(dtype, out_dtype)) {
+    const MapSource t[3] = {{q, d_k, q_stride}, {k, d_k, k_stride}, {v, d_v, v_stride}};
+    encode_maps(a, t, 3, scan_mode);
+  }
+  const Cut c = cut_for(B, H, L, d_k, d_v, on_tc(dtype, out_dtype), cu_seqlens != nullptr, 1);
   return launch(a, 1, c, workspace, dtype, out_dtype, static_cast<cudaStream_t>(stream));
 }
 
@@ -181,10 +217,14 @@ dig_status dig_decay_attn_bwd(const void* q, const void* k, const void* v, long 
   a.B = B, a.H = H, a.L = L, a.Hg = grid_h, a.Wg = grid_w;
   const long long os = (long long)H * d_v;
   const int rev = scan_mode ^ 1;
-  a.p[0] = DecayProblem{dO, v, k, dq, os, v_stride, k_stride, S0, nullptr, d_v, d_k, 1, 0, scan_mode, scale, 1.f, scale};
-  a.p[1] = DecayProblem{k, q, dO, dv, k_stride, q_stride, os, dS_final, dS0, d_k, d_v, 0, 1, rev, scale, scale, 1.f};
-  a.p[2] = DecayProblem{v, dO, q, dk, v_stride, os, q_stride, dS_final, nullptr, d_v, d_k, 1, 1, rev, scale, scale, 1.f};
-  const Cut c = cut_for(B, H, L, d_k, d_v, dtype, cu_seqlens != nullptr, 3);
+  a.p[0] = DecayProblem{dO, v, k, dq, os, v_stride, k_stride, S0, nullptr, d_v, d_k, 1, 0, scan_mode, scale, 1.f, scale, 3, 2, 1};
+  a.p[1] = DecayProblem{k, q, dO, dv, k_stride, q_stride, os, dS_final, dS0, d_k, d_v, 0, 1, rev, scale, scale, 1.f, 1, 0, 3};
+  a.p[2] = DecayProblem{v, dO, q, dk, v_stride, os, q_stride, dS_final, nullptr, d_v, d_k, 1, 1, rev, scale, scale, 1.f, 2, 3, 0};
+  if (on_tc(dtype, out_dtype)) {
+    const MapSource t[4] = {{q, d_k, q_stride}, {k, d_k, k_stride}, {v, d_v, v_stride}, {dO, d_v, os}};
+    encode_maps(a, t, 4, scan_mode);
+  }
+  const Cut c = cut_for(B, H, L, d_k, d_v, on_tc(dtype, out_dtype), cu_seqlens != nullptr, 3);
   return launch(a, 3, c, workspace, dtype, out_dtype, static_cast<cudaStream_t>(stream));
 }
 

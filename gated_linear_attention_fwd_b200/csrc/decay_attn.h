@@ -16,6 +16,7 @@
 // segment's own state contribution (segment 0: with S0 in it), and the second
 // one joins those before its segment into the state it starts from.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "dig_common.cuh"
@@ -33,9 +34,16 @@ struct DecayProblem {
   int lag;
   int mode;
   float a, b, c;
+  int mq, mk, mv;  // the tensors' maps in DecayArgs::map
 };
 
+// How the tensor-core kernel fetches tiles: token by token, or by TMA from whole-row or column maps.
+enum { kFetchTokens = 0, kFetchRows = 1, kFetchCols = 2 };
+constexpr int kColRun = 16;  // tokens of a column map's box
+
 struct DecayArgs {
+  alignas(64) CUtensorMap map[4];
+  int fetch;
   DecayProblem p[3];
   const float* g;  // [H] log decays
   const int* cu;
@@ -139,5 +147,6 @@ __device__ __forceinline__ float2 decay_pow(float g, long long i) {
 // Launches of the two passes (states: only where a sequence has more than one segment).
 cudaError_t launch_decay_f32(const DecayArgs& a, int nprob, int nseg_total, bool multi, int D, int dtype, int out_dtype,
                              cudaStream_t s);
+cudaError_t launch_decay_tc(const DecayArgs& a, int nprob, int nseg_total, bool multi, int D, cudaStream_t s);
 
 }  // namespace dig

@@ -1,0 +1,709 @@
+// decay_attn_tc.cu -- head-decay linear attention on the tensor core (bf16 inputs
+// and outputs).
+//
+// One block walks a segment of one (sequence, head) in chunks of 128 tokens; per
+// chunk (n tokens, entry state S, the problem's factors a, b, c):
+//   P  = q k^T,            P[t][s] <- a lambda^(t-s) P[t][s] for s <= t, else 0
+//   dS = khat^T v,         khat_s = b lambda^(n-1-s) k_s
+//   O1 = q S,              O2 = P v,      o[t] = c lambda^(t+1) O1[t] + O2[t]
+//   S  = lambda^n S + dS
+// all four products by tcgen05.mma with fp32 accumulators in tensor memory.  One
+// warp issues them, three more fetch a tile each, and the rest (4 warps per 32
+// lanes at D = 128, 2 at D = 64, so that a thread holds 32 columns of S, dS and O
+// either way) do what is between the products:
+//   - q, k, v tiles (raw bf16, exact) come two chunks deep into 128-byte-swizzled
+//     tiles of 64 channels, by TMA (boxes of whole rows, or of runs of a grid
+//     column; a reversed scan keeps its tiles in memory order and mirrors the mask)
+//     or, where alignment or the grid does not allow that, token by token through
+//     cp.async.  Rows past the segment and channels past the head are zero.  The same
+//     bytes serve K-major (q k^T) and MN-major (v as the second operand);
+//   - P is masked, scaled and split into two bf16 terms in place in tensor memory
+//     and read from there as the first operand of P v.  The decays are applied to
+//     the fp32 product (lambda^(t-s) itself, no quotient of powers: any lambda from
+//     0 to 1 is in range);
+//   - S lives in fp32 registers (one key channel per lane) and is left in shared
+//     memory as one bf16 term, the second operand of q S: off by at most half a
+//     bf16 step, as the output's own rounding is (a second term has no room beside
+//     two chunks of tiles).  lambda^n is applied as hi + lo and dS is summed apart
+//     from S: a tensor-core accumulator that carried S through the sequence would
+//     cut a little off it at every addition;
+//   - khat^T (lane = channel) goes to tensor memory through transposing matrix
+//     loads: two bf16 terms where the state only feeds outputs, three, exact to
+//     fp32, where the final state itself is asked for.
+// Products run in the order of their issue, which lets them share columns: khat
+// lies where O1 (D = 128; its third term in the other P) or P and O1 (D = 64) come
+// to stand, and O2 where dS stood.  At D = 128 there are two P, and q k^T of the
+// next chunk is issued ahead of P v.
+#include <cuda_bf16.h>
+
+#include "decay_attn.h"
+#include "sm100.cuh"
+#include "tma.cuh"
+
+namespace dig {
+
+namespace {
+
+constexpr int C = 128;  // tokens of a chunk
+
+// 16 consecutive columns of this thread's lane, loaded and waited for in one statement (no use can move above the wait).
+__device__ __forceinline__ void tmem_take16(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+// 16 lanes x 16 columns: register 2 i (2 i + 1) of thread T is lane T / 4 (+ 8), column 4 i + T % 4, the
+// arrangement in which transposing matrix loads leave a tile.
+__device__ __forceinline__ void tmem_put_16x16(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// Four 8 x 8 matrices of 16-bit values, each transposed: thread T gets row T / 4, values 2 (T % 4) and + 1 of each.
+__device__ __forceinline__ void ldsm_t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+// One row piece of 16 or 8 bytes; nothing is read and zeros are written where `bytes` is 0.
+template <int N>
+__device__ __forceinline__ void cp_piece(uint32_t dst, const void* src, int bytes) {
+  if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// Barrier `id` over `n` threads; true for all of them if `x` is for any.
+__device__ __forceinline__ bool bar_or(int id, int n, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(x ? 1u : 0u), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 x;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 x;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(addr) : "memory");
+  return x;
+}
+// Moves registers between the warps of a block (warpgroup-wide; the sums stay within the launch's total).
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// The next bf16 term of a pair of values: packed, and taken off the values.
+__device__ __forceinline__ uint32_t take_term(float& x, float& y) {
+  const uint32_t t = pack_bf16x2(x, y);
+  x -= __uint_as_float(t << 16);
+  y -= __uint_as_float(t & 0xFFFF0000u);
+  return t;
+}
+
+// Second operand read MN-major: rows are the contracted index, atoms of 64 columns `atom` bytes apart.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t atom) {
+  uint64_t d = sdesc_sw<128>(addr);
+  d &= ~(static_cast<uint64_t>(0x3FFF) << 16);
+  return d | static_cast<uint64_t>((atom >> 4) & 0x3FFF) << 16;
+}
+
+enum { kFull, kLast, kFullLag, kLastLag, kSegment, kSteps };
+
+template <int D, bool STATES>
+struct TcCfg {
+  static constexpr bool SMALL = D == 64;
+  static constexpr int CG = D / 32;               // threads per lane
+  static constexpr int NT = 128 * CG;             // worker threads; 128 more issue and fetch
+  static constexpr int ATOM = C * 128;            // bytes of 64 channels of a tile
+  static constexpr int TILE = ATOM * (D / 64);
+  static constexpr int PER = STATES ? 2 : 3;      // tiles of a chunk: k, v, q
+  static constexpr int S_ATOM = D * 128;
+  static constexpr int OFF_S = PER * 2 * TILE;
+  static constexpr int OFF_T = OFF_S + (STATES ? 0 : S_ATOM * (D / 64));
+  // registers: 512 x 104 + 128 x 56 of 640 x 96 (D = 128), 256 x 96 + 128 x 48 of 384 x 80 (D = 64)
+  static constexpr int REGS = SMALL ? 96 : 104, REGS_SERVICE = SMALL ? 48 : 56;
+  // tensor memory columns
+  static constexpr int TM_COLS = SMALL ? 256 : 512;
+  static constexpr int TM_O1 = SMALL ? 128 : 256, TM_DS = SMALL ? 192 : 384, TM_O2 = TM_DS;
+  static constexpr int PW = C / CG;               // P columns of a thread
+  // first column of P of chunk m
+  __device__ static __forceinline__ uint32_t tm_p(int m) { return SMALL ? 0 : (m & 1) * 128; }
+  // first column of term i (64 columns) of khat of chunk m
+  __device__ static __forceinline__ uint32_t tm_k(int m, int i) {
+    if (SMALL) return 64 * i;
+    if (STATES) return (m & 1) * 192 + 64 * i;
+    return i < 2 ? TM_O1 + 64 * i : ((m + 1) & 1) * 128;
+  }
+};
+
+struct TcTables {
+  float pw[C + 4];                  // lambda^i
+  float2 step[kSteps];              // lambda^i = hi + lo of a chunk's or segment's tokens
+  float p16[16];                    // lambda^(15-i), mirrored tiles: lambda^i
+  float wk[2][C];                   // b lambda^(n-1-s) of chunk m in m & 1, 0 past its end
+  uint64_t full[2];                 // the chunk's tiles have come
+  uint64_t landed[2];               // k and v of a chunk that ends inside its tiles
+  uint64_t free_[3][2];             // tile x (k, v, q) of the chunk is no longer read
+  uint64_t bar_k, bar_p;            // the workers': khat (with S) written, P written (and dS read)
+  uint64_t bar_qk[2], bar_ds, bar_qs, bar_pv, bar_end;  // the tensor core's
+  uint32_t tmem;
+  int abort;
+};
+
+// What a segment's block does: STATES, the segment's own contribution to the state; else its outputs.
+template <int D, bool STATES>
+__global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) decay_tc_kernel(const __grid_constant__ DecayArgs a) {
+  using F = TcCfg<D, STATES>;
+  static_assert(F::OFF_T + sizeof(TcTables) <= (D == 64 ? 113 : 227) * 1024, "the blocks of an SM fit its shared memory");
+  constexpr int NT = F::NT, CG = F::CG, W0 = NT / 32;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  TcTables& sh = *reinterpret_cast<TcTables*>(smem + F::OFF_T);
+  const int tid = threadIdx.x, warp = tid >> 5, ln = tid & 31;
+  const int h = blockIdx.y;
+  const DecayProblem& p = a.p[blockIdx.z];
+  const uint32_t sb = smem_u32(smem);
+  if (warp == W0) {
+    tmem_alloc(&sh.tmem, F::TM_COLS);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.full[i], F::PER);
+      mbar_init(&sh.free_[0][i], 1);
+      mbar_init(&sh.free_[1][i], 1);
+      mbar_init(&sh.free_[2][i], NT / 32);
+      mbar_init(&sh.bar_qk[i], 1);
+    }
+    mbar_init(&sh.bar_k, NT / 32);
+    mbar_init(&sh.bar_p, NT / 32);
+    mbar_init(&sh.bar_ds, 1);
+    mbar_init(&sh.bar_qs, 1);
+    mbar_init(&sh.bar_pv, 1);
+    mbar_init(&sh.bar_end, 1);
+    mbar_init(&sh.landed[0], 1);
+    mbar_init(&sh.landed[1], 1);
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  if (!STATES && a.cu && blockIdx.x == 0 && h == 0 && blockIdx.z == 0 && warp == 0) decay_check_offsets(a);
+  const float g = a.g[h];
+  // tile row i holds scan position i of the chunk, or 127 - i where a reversed scan's tiles stay in memory order
+  const bool rev = a.fetch != kFetchTokens && (p.mode & 1);
+  DecayUnit u;
+  bool on = decay_unit(a, blockIdx.x, u);
+  if (tid < C + kSteps) {
+    // threads C ..: lambda to the tokens of a whole chunk, of the last one, of either where its first token counts
+    // without its decay (lag), and of a segment
+    const int last = on ? u.n - max(u.n - 1, 0) / C * C : 0;
+    const int i = tid <= C ? tid : (tid == C + kLast ? last : (tid == C + kFullLag ? C - 1 : (tid == C + kLastLag ? max(last - 1, 0) : a.seg)));
+    const float2 w = decay_pow(g, i);
+    if (tid <= C) sh.pw[tid] = w.x;
+    if (tid >= C) sh.step[tid - C] = w;
+    if (tid < 16) sh.p16[rev ? tid : 15 - tid] = w.x;
+  }
+  if (STATES && on) on = u.nseg > 1 && u.i < u.nseg - 1;  // a last segment's state is formed by the output pass
+  if (sb & 1023u) {  // the swizzled tiles start at 1024-byte boundaries
+    set_status(a.status, DIG_ERR_CUDA);
+    on = false;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  if (!on) {
+    if (warp == W0) tmem_dealloc(tmem, F::TM_COLS);
+    return;
+  }
+  const int nch = (u.n + C - 1) / C;
+  const int terms = p.Sf && u.slot >= 0 ? 3 : 2;  // of khat
+  const int kk = (p.dk + 15) / 16;                // K-steps over the key channels
+  const int nv = (p.dv + 15) / 16 * 16;           // columns of the products with v or S
+  auto tile = [&](int x, int m) { return sb + ((m & 1) * F::PER + x) * F::TILE; };  // x: 0 k, 1 v, 2 q
+  // Waits are bounded (2^20 probes, far beyond any legitimate wait); after one gave up every other one does, nothing
+  // more is issued and the block leaves.
+  bool timed_out = false;
+  auto wait_bar = [&](uint64_t* bar, uint32_t parity) {
+    for (uint32_t i = 0; !timed_out && !mbar_try_wait(bar, parity); ++i) {
+      if (*reinterpret_cast<volatile int*>(&sh.abort)) return false;
+      if (i == 1u << 20) {
+        timed_out = true;
+        sh.abort = 1;
+      }
+    }
+    return !timed_out;
+  };
+
+  if (warp >= W0) {
+   regs_down<F::REGS_SERVICE>();
+   if (warp == W0) {
+    // ---- the issuing warp
+    if (ln == 0) {
+      const uint32_t id_qk = idesc_bf16(128, 128), id_v = idesc_bf16(128, nv, false, true);
+      const uint64_t s_desc = mn_desc(sb + F::OFF_S, F::S_ATOM);
+      auto kstep = [&](int ks) { return (uint64_t)(((ks >> 2) * F::ATOM + (ks & 3) * 32) >> 4); };
+      auto qk = [&](int m) {
+        const uint64_t kd = sdesc_sw<128>(tile(0, m)), qd = sdesc_sw<128>(tile(2, m));
+#pragma unroll 2
+        for (int ks = 0; ks < kk; ++ks) mma_bf16(tmem + F::tm_p(m), qd + kstep(ks), kd + kstep(ks), id_qk, ks ? 1u : 0u);
+        mma_commit(&sh.bar_qk[m & 1]);
+      };
+      int done = 0;  // chunks whose q k^T is issued
+      if (!STATES && !F::SMALL && nch > 0 && wait_bar(&sh.full[0], 0)) {
+        qk(0);
+        done = 1;
+      }
+      for (int m = 0; m < nch; ++m) {
+        const uint32_t ph = m & 1;
+        if (!wait_bar(&sh.full[m & 1], (m >> 1) & 1) || !wait_bar(&sh.bar_k, ph)) break;
+        tc_fence_after();
+        if (!STATES && !F::SMALL && done == m) qk(m), done = m + 1;
+        const uint64_t v0 = mn_desc(tile(1, m), F::ATOM);
+#pragma unroll 1
+        for (int i = terms - 1; i >= 0; --i)  // the smallest terms first
+#pragma unroll 2
+          for (int ks = 0; ks < C / 16; ++ks)
+            mma_bf16_ts(tmem + F::TM_DS, tmem + F::tm_k(m, i) + 8 * ks, v0 + (uint64_t)((2048 * ks) >> 4), id_v,
+                        ks == 0 && i == terms - 1 ? 0u : 1u);
+        mma_commit(&sh.bar_ds);
+        if (STATES) {
+          mma_commit(&sh.free_[0][m & 1]);
+          mma_commit(&sh.free_[1][m & 1]);
+        } else {
+          if (F::SMALL) qk(m);
+          mma_commit(&sh.free_[0][m & 1]);
+          const uint64_t qd = sdesc_sw<128>(tile(2, m));
+#pragma unroll 2
+          for (int ks = 0; ks < kk; ++ks)
+            mma_bf16(tmem + F::TM_O1, qd + kstep(ks), s_desc + (uint64_t)((2048 * ks) >> 4), id_v, ks ? 1u : 0u);
+          mma_commit(&sh.bar_qs);
+          if (!F::SMALL && m + 1 < nch && mbar_test_wait(&sh.full[(m + 1) & 1], ((m + 1) >> 1) & 1)) qk(m + 1), done = m + 2;
+          if (!wait_bar(&sh.bar_p, ph)) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int i = 1; i >= 0; --i)  // a K-step's 16 columns: 8 of the first term, 8 of the second
+#pragma unroll 2
+            for (int ks = 0; ks < C / 16; ++ks)
+              mma_bf16_ts(tmem + F::TM_O2, tmem + F::tm_p(m) + 16 * ks + 8 * i, v0 + (uint64_t)((2048 * ks) >> 4), id_v,
+                          i == 1 && ks == 0 ? 0u : 1u);
+          mma_commit(&sh.bar_pv);
+          mma_commit(&sh.free_[1][m & 1]);
+        }
+      }
+      mma_commit(&sh.bar_end);  // no product outlives the block
+      mbar_wait(&sh.bar_end, 0, kSpinLimitNs);
+    }
+    __syncwarp();
+   } else {
+    // ---- the fetching warps: tile x of each chunk, in 16-byte pieces where all strides allow it, else in 8-byte ones
+    const int x = warp - W0 - 1;
+    if (x < F::PER) {
+      const bool wide = (p.dk | p.dv) % 8 == 0 && (p.qs | p.ks | p.vs) % 8 == 0 &&
+                        ((reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v)) & 15) == 0;
+      const int d = x == 1 ? p.dv : p.dk;
+      const long long st = 2 * (x == 0 ? p.ks : (x == 1 ? p.vs : p.qs));
+      const char* base = static_cast<const char*>(x == 0 ? p.k : (x == 1 ? p.v : p.q)) + (size_t)h * d * 2;
+      auto fetch = [&](int m) {
+        const uint32_t dst = tile(x, m);
+        const int n = min(C, u.n - m * C);
+        if (x == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int s = rev ? C - 1 - 32 * i - ln : 32 * i + ln;
+            sh.wk[m & 1][32 * i + ln] = s < n ? p.b * sh.pw[n - 1 - s] : 0.f;
+          }
+        }
+        if (a.fetch != kFetchTokens) {
+          const CUtensorMap& map = a.map[x == 0 ? p.mk : (x == 1 ? p.mv : p.mq)];
+          // packed: rows past the sequence's end are another's, and 0 times them need not be 0
+          const bool clean = x < 2 && a.cu && n < C;
+          uint64_t* bar = clean ? &sh.landed[x] : &sh.full[m & 1];
+          const int atoms = min(D / 64, (d + 63) / 64);
+          __syncwarp();
+          if (ln == 0) {
+            mbar_arrive_expect_tx(bar, atoms * F::ATOM);
+            const int t0 = u.t0 + m * C;
+            if (a.fetch == kFetchRows) {
+              const int r = (rev ? u.len - t0 - C : t0) + (a.cu ? u.first : 0);
+              for (int i = 0; i < atoms; ++i) tma_load_5d(dst + i * F::ATOM, map, 64 * i, h, r, a.cu ? 0 : u.b, 0, bar);
+            } else {
+              const int f0 = rev ? a.L - t0 - C : t0;  // a multiple of the run, as L and the segments are
+              int col = f0 >= 0 ? f0 / a.Hg : 0, y = f0 >= 0 ? f0 - col * a.Hg : f0;
+              for (int r = 0; r < C; r += kColRun) {
+                const int yy = y < 0 ? a.Hg : y;  // before the first token: off the grid, zeros
+                for (int i = 0; i < atoms; ++i) tma_load_5d(dst + i * F::ATOM + r * 128, map, 64 * i, h, yy, col, u.b, bar);
+                y += kColRun;
+                if (y >= a.Hg) y = 0, ++col;
+              }
+            }
+          }
+          if (clean) {
+            wait_bar(&sh.landed[x], 0);
+            const int r0 = rev ? 0 : n, rows = C - n;
+            for (int i = ln; i < rows * 8; i += 32)
+              for (int j = 0; j < atoms; ++j) sts128(dst + j * F::ATOM + (r0 + i / 8) * 128 + (i % 8) * 16, 0, 0, 0, 0);
+            fence_async_smem();
+            __syncwarp();
+            if (ln == 0) mbar_arrive(&sh.full[m & 1]);
+          }
+          return;
+        }
+        int row[4];  // of tokens ln, ln + 32, ..
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int s = m * C + 32 * i + ln;
+          row[i] = s < u.n ? decay_row(a, u, p.mode, u.t0 + s) : -1;
+        }
+        auto go = [&](auto bytes) {
+          constexpr int N = decltype(bytes)::value, PR = D * 2 / N, RW = PR < 32 ? 32 / PR : 1;  // pieces of a row, rows at once
+          const int c = (ln % PR) * (N / 2);
+          const bool any = c < (d + 15) / 16 * 16, in = c < d;  // columns that a product reads; that exist
+          const uint32_t cdst = dst + (c >> 6) * F::ATOM + (N == 16 ? 0u : (c & 4) * 2u);
+          const int ch = (c & 63) >> 3;
+          const char* cb = base + 2 * c;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll 2
+            for (int r0 = 0; r0 < 32; r0 += RW) {
+              const int r = r0 + ln / PR;
+              const int gr = __shfl_sync(0xFFFFFFFFu, row[i], r);
+              const bool ok = in && gr >= 0;
+              if (any) cp_piece<N>(cdst + (32 * i + r) * 128 + ((ch ^ (r & 7)) << 4), ok ? cb + gr * st : base, ok ? N : 0);
+            }
+        };
+        if (wide) go(std::integral_constant<int, 16>{});
+        else go(std::integral_constant<int, 8>{});
+        cp_commit();
+        cp_wait<0>();
+        fence_async_smem();
+        __syncwarp();
+        if (ln == 0) mbar_arrive(&sh.full[m & 1]);
+      };
+#pragma unroll 1
+      for (int m = 0; m < nch; ++m) {
+        if (m >= 2 && __any_sync(0xFFFFFFFFu, !wait_bar(&sh.free_[x][m & 1], ((m - 2) >> 1) & 1))) break;
+        fetch(m);
+      }
+    }
+   }
+  } else {
+    regs_up<F::REGS>();
+    const int t = tid & 127, cg = tid >> 7;  // token row or key channel (the thread's TMEM lane); column group
+    const uint32_t lane = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const bool key = t < D && t < p.dk;      // this lane holds a key channel of the state
+    auto arrive = [&](uint64_t* bar) {       // the warp's writes to tensor and shared memory are done
+      fence_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (ln == 0) mbar_arrive(bar);
+    };
+
+    // ---- the state the segment starts from: lane t = key channel, value channels 32 cg ..
+    float S[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) S[j] = 0.f;
+    float* seg_base = a.segst + blockIdx.z * a.segst_problem;
+    const int seg0 = blockIdx.x - u.i;
+    // element (c, j) of a segment state: four value channels of consecutive key channels side by side
+    auto seg_state = [&](int sidx) {
+      return reinterpret_cast<float4*>(seg_base + ((size_t)sidx * a.H + h) * (D * D)) + (cg * 8) * D + t;
+    };
+    if (t < D) {
+      if (u.i == 0 && (STATES || u.nseg == 1)) {
+        if (p.S0 && u.slot >= 0 && key) {
+          const float* s0 = p.S0 + ((size_t)u.slot * a.H + h) * p.dk * p.dv;
+          if (p.s0_t) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (cg * 32 + j < p.dv) S[j] = s0[(size_t)(cg * 32 + j) * p.dk + t];
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              if (cg * 32 + j < p.dv) {
+                const float4 x = *reinterpret_cast<const float4*>(s0 + (size_t)t * p.dv + cg * 32 + j);
+                S[j] = x.x, S[j + 1] = x.y, S[j + 2] = x.z, S[j + 3] = x.w;
+              }
+          }
+        }
+      } else if (!STATES && u.i == 0) {  // the copy of S0 that the first pass left (S0 may be overwritten by the last segment)
+        const float4* s0 = seg_state(seg0 + u.nseg - 1);
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 x = s0[(j / 4) * D];
+          S[j] = x.x, S[j + 1] = x.y, S[j + 2] = x.z, S[j + 3] = x.w;
+        }
+      } else if (!STATES) {
+        const float2 w = sh.step[kSegment];
+#pragma unroll 2
+        for (int m = 0; m < u.i; ++m) {
+          const float4* ls = seg_state(seg0 + m);
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 x = ls[(j / 4) * D];
+            S[j] = fmaf(w.x, S[j], fmaf(w.y, S[j], x.x));
+            S[j + 1] = fmaf(w.x, S[j + 1], fmaf(w.y, S[j + 1], x.y));
+            S[j + 2] = fmaf(w.x, S[j + 2], fmaf(w.y, S[j + 2], x.z));
+            S[j + 3] = fmaf(w.x, S[j + 3], fmaf(w.y, S[j + 3], x.w));
+          }
+        }
+      }
+      if (STATES && u.i == 0) {
+        float4* s0 = seg_state(seg0 + u.nseg - 1);  // the last segment's place is free: it leaves no state there
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) s0[(j / 4) * D] = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+      }
+    }
+    // S in bf16, rows = key channels (64 value channels each), the second operand of q S
+    auto put_state = [&]() {
+      if (t < D) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+          const int jj = cg * 32 + j;
+          sts128(sb + F::OFF_S + (jj >> 6) * F::S_ATOM + swz_off<128>(t, (jj & 63) >> 3), pack_bf16x2(S[j], S[j + 1]),
+                 pack_bf16x2(S[j + 2], S[j + 3]), pack_bf16x2(S[j + 4], S[j + 5]), pack_bf16x2(S[j + 6], S[j + 7]));
+        }
+      }
+    };
+    if constexpr (!STATES) put_state();
+    // khat^T of chunk m -> tensor memory: the warp's 32 channels, its group's tokens
+    auto convert_k = [&](int m) {
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        const int c = 32 * (warp & 3) + 16 * half;
+        if (c >= 16 * kk) break;
+        const uint32_t kt = tile(0, m) + (c >> 6) * F::ATOM;
+        const int ch = ((c & 63) >> 3) + ((ln >> 3) & 1);
+#pragma unroll 1
+        for (int s0 = cg * F::PW; s0 < (cg + 1) * F::PW; s0 += 32) {
+          uint32_t r[8];
+          float x[16];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int tok = s0 + 16 * i + ((ln >> 4) << 3) + (ln & 7);
+            ldsm_t(kt + tok * 128 + ((ch ^ (tok & 7)) << 4), r + 4 * i);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 w = *reinterpret_cast<const float2*>(&sh.wk[m & 1][s0 + 8 * i + 2 * (ln & 3)]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              x[4 * i + 2 * e] = __uint_as_float(r[2 * i + e] << 16) * w.x;
+              x[4 * i + 2 * e + 1] = __uint_as_float(r[2 * i + e] & 0xFFFF0000u) * w.y;
+            }
+          }
+          const uint32_t at = tmem + (static_cast<uint32_t>(c) << 16) + s0 / 2;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) r[i] = take_term(x[2 * i], x[2 * i + 1]);
+          tmem_put_16x16(at + F::tm_k(m, 0), r);
+          if (terms == 3) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] = take_term(x[2 * i], x[2 * i + 1]);
+            tmem_put_16x16(at + F::tm_k(m, 1), r);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) r[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+          tmem_put_16x16(at + F::tm_k(m, terms - 1), r);
+        }
+      }
+      tmem_st_wait();
+    };
+    // S = lambda^n S + dS (columns past nv hold nothing that is read)
+    auto update = [&](int n, int e) {
+      if (32 * (warp & 3) < D) {
+        const float2 w = sh.step[(n < C ? kLast : kFull) + (e ? kFullLag - kFull : 0)];
+#pragma unroll
+        for (int j = 0; j < 32; j += 16) {
+          float x[16];
+          tmem_take16(tmem + lane + F::TM_DS + 32 * cg + j, x);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) S[j + i] = fmaf(w.x, S[j + i], fmaf(w.y, S[j + i], x[i]));
+        }
+      }
+    };
+    // P of chunk m: masked, scaled, two bf16 terms in place (each 16 columns: 8 of the first, 8 of the second)
+    auto convert_p = [&](int m) {
+      const int tb = 32 * (warp & 3);
+#pragma unroll 1
+      for (int b = 0; b < F::PW; b += 16) {
+        const int s0 = cg * F::PW + b;
+        uint32_t w[16];
+        if (rev ? s0 + 15 < tb : s0 > tb + 31) {  // later positions only
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = 0u;
+        } else {
+          float x[16];
+          tmem_take16(tmem + lane + F::tm_p(m) + s0, x);
+          if (rev ? s0 >= tb + 31 : s0 + 15 <= tb) {  // earlier ones only: lambda^(t - s) = lambda^(t - s0 - 15) lambda^(15 - i)
+            const float base = p.a * sh.pw[rev ? s0 - t : t - s0 - 15];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] *= base * sh.p16[i];
+          } else {
+            const int d = t - s0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int k = rev ? i - d : d - i;
+              x[i] = k >= 0 ? x[i] * (p.a * sh.pw[max(k, 0)]) : 0.f;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            w[i] = take_term(x[2 * i], x[2 * i + 1]);
+            w[8 + i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+          }
+        }
+        tmem_st16(tmem + lane + F::tm_p(m) + s0, w);
+      }
+      tmem_st_wait();
+    };
+    // The warp's 32 rows x 32 columns of the output, through its 2 KB of the q tile, to whole 64-byte pieces of rows
+    auto put_out = [&](int m, int e) {
+      const int jj = 32 * cg;
+      if (jj >= nv) return;
+      const int s = rev ? C - 1 - t : t;
+      const float f = p.c * sh.pw[s + 1 - e];
+      const uint32_t st = tile(2, m) + warp * 2048;
+#pragma unroll
+      for (int j = 0; j < 32; j += 16) {
+        float x[16], y[16];
+        tmem_take16(tmem + lane + F::TM_O1 + jj + j, x);
+        tmem_take16(tmem + lane + F::TM_O2 + jj + j, y);
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(fmaf(f, x[2 * i], y[2 * i]), fmaf(f, x[2 * i + 1], y[2 * i + 1]));
+        sts128(st + swz_off<64>(ln, j / 8), w[0], w[1], w[2], w[3]);
+        sts128(st + swz_off<64>(ln, j / 8 + 1), w[4], w[5], w[6], w[7]);
+      }
+      __syncwarp();
+      const int row = m * C + s < u.n ? decay_row(a, u, p.mode, u.t0 + m * C + s) : -1;
+      char* o = static_cast<char*>(p.o) + ((size_t)h * p.dv + jj) * 2;
+      const size_t os = (size_t)a.H * p.dv * 2;
+      const int left = p.dv - jj;
+      if (p.dv % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+          const int r = i + ln / 4, gr = __shfl_sync(0xFFFFFFFFu, row, r);
+          const uint4 v = lds128(st + swz_off<64>(r, ln & 3));
+          if (gr >= 0 && 8 * (ln & 3) < left) *reinterpret_cast<uint4*>(o + gr * os + 16 * (ln & 3)) = v;
+        }
+      } else {
+#pragma unroll 2
+        for (int i = 0; i < 32; i += 4) {
+          const int r = i + ln / 8, gr = __shfl_sync(0xFFFFFFFFu, row, r);
+          const uint2 v = lds64(st + swz_off<64>(r, (ln & 7) >> 1) + 8 * (ln & 1));
+          if (gr >= 0 && 4 * (ln & 7) < left) *reinterpret_cast<uint2*>(o + gr * os + 8 * (ln & 7)) = v;
+        }
+      }
+    };
+
+    if constexpr (STATES) {
+      // khat of the next chunk is formed while the tensor core sums this one's dS (D = 128: two places for it)
+      constexpr bool AHEAD = !F::SMALL;
+      for (int m = 0; m < nch + (AHEAD ? 1 : 0); ++m) {
+        if (m < nch) {
+          wait_bar(&sh.full[m & 1], (m >> 1) & 1);
+          if (__any_sync(0xFFFFFFFFu, timed_out || *reinterpret_cast<volatile int*>(&sh.abort))) break;
+          convert_k(m);
+        }
+        const int j = AHEAD ? m - 1 : m;
+        if (!AHEAD) arrive(&sh.bar_k);
+        if (j >= 0) {
+          wait_bar(&sh.bar_ds, j & 1);
+          tc_fence_after();
+          update(min(C, u.n - j * C), p.lag && u.t0 + j * C == 0 ? 1 : 0);
+        }
+        if (AHEAD && m < nch) arrive(&sh.bar_k);
+      }
+      if (t < D) {
+        float4* out = seg_state(blockIdx.x);
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) out[(j / 4) * D] = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+      }
+    } else {
+      for (int m = 0; m < nch; ++m) {
+        const uint32_t ph = m & 1;
+        const int n = min(C, u.n - m * C);
+        const int e = (p.lag && u.t0 + m * C == 0) ? 1 : 0;
+        wait_bar(&sh.full[m & 1], (m >> 1) & 1);
+        // the warps of these lanes have read the last chunk's outputs, where khat comes to stand
+        if (bar_or(1 + (warp & 3), 32 * CG, timed_out || *reinterpret_cast<volatile int*>(&sh.abort))) break;
+        convert_k(m);
+        arrive(&sh.bar_k);
+        if (!F::SMALL) {
+          wait_bar(&sh.bar_qk[m & 1], (m >> 1) & 1);
+          tc_fence_after();
+          convert_p(m);
+        }
+        wait_bar(&sh.bar_ds, ph);
+        tc_fence_after();
+        update(n, e);  // before P v, which comes to stand in dS's place
+        if (F::SMALL) {
+          wait_bar(&sh.bar_qk[m & 1], (m >> 1) & 1);
+          tc_fence_after();
+          convert_p(m);
+        }
+        arrive(&sh.bar_p);
+        wait_bar(&sh.bar_qs, ph);
+        put_state();
+        wait_bar(&sh.bar_pv, ph);
+        tc_fence_after();
+        put_out(m, e);
+        fence_async_smem();  // the next tile comes over what was staged there
+        __syncwarp();
+        if (ln == 0) mbar_arrive(&sh.free_[2][m & 1]);
+      }
+      if (p.Sf && u.slot >= 0 && u.i == u.nseg - 1 && key) {
+        // dS0 = lambda G_0; an empty sequence passes its state on as it is
+        const float w = p.lag && u.len > 0 ? sh.pw[1] : 1.f;
+        float* out = p.Sf + ((size_t)u.slot * a.H + h) * p.dk * p.dv + (size_t)t * p.dv + cg * 32;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4)
+          if (cg * 32 + j < p.dv) *reinterpret_cast<float4*>(out + j) = make_float4(w * S[j], w * S[j + 1], w * S[j + 2], w * S[j + 3]);
+      }
+    }
+  }
+  if (timed_out) set_status(a.status, DIG_ERR_DEVICE_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == W0) tmem_dealloc(tmem, F::TM_COLS);
+}
+
+template <int D, bool STATES>
+cudaError_t run(const DecayArgs& a, dim3 grid, cudaStream_t s) {
+  using F = TcCfg<D, STATES>;
+  constexpr int smem = F::OFF_T + sizeof(TcTables);
+  const cudaError_t e = cudaFuncSetAttribute(decay_tc_kernel<D, STATES>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(decay_tc_kernel<D, STATES>, grid, dim3(F::NT + 128), smem, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_decay_tc(const DecayArgs& a, int nprob, int nseg_total, bool multi, int D, cudaStream_t s) {
+  const dim3 grid(nseg_total, a.H, nprob);
+  cudaError_t e;
+  if (multi && (e = D == 64 ? run<64, true>(a, grid, s) : run<128, true>(a, grid, s)) != cudaSuccess) return e;
+  return D == 64 ? run<64, false>(a, grid, s) : run<128, false>(a, grid, s);
+}
+
+}  // namespace dig

@@ -59,4 +59,17 @@ bool tmap_cols(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esi
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool tmap_heads(CUtensorMap* m, const void* base, int d, int H, const uint64_t len[3], const uint64_t stride[3],
+                uint32_t box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[5] = {(cuuint64_t)d, (cuuint64_t)H, len[0], len[1], len[2]};
+  const cuuint64_t strides[4] = {2 * (cuuint64_t)d, 2 * stride[0], 2 * stride[1], 2 * stride[2]};
+  const cuuint32_t box[5] = {64, 1, box_rows, 1, 1};
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace dig

@@ -19,5 +19,9 @@ bool tmap_rows(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esi
                uint64_t rows, uint32_t box_elems, uint32_t box_rows, int rb);
 bool tmap_cols(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize, uint64_t row_elems, int Hg, int Wg,
                int B, uint32_t box_elems, uint32_t box_rows, int rb);
+// bf16 heads of d values (H dense heads a token) under three token axes of the given lengths and strides (in
+// elements); a box is 64 channels of one head at `box_rows` places of the first axis, in the 128-byte swizzle.
+bool tmap_heads(CUtensorMap* m, const void* base, int d, int H, const uint64_t len[3], const uint64_t stride[3],
+                uint32_t box_rows);
 
 }  // namespace dig

@@ -59,10 +59,11 @@ def attn_bound(size, longest, dk, dv, bf16):
 
     Every output is a sum of products q k v lambda^n.  A chain of at most dk + dv + 2 longest + 64 roundings of
     2^-23 at most (a tensor-core addition may cut instead of rounding; the decays cost a few more) leads to it.
-    With bf16 inputs the masked products and the state enter their second product as two bf16 terms each, which is
-    off by at most (2^-8)^2 of the term."""
+    With bf16 inputs and outputs the masked products, the state and the decayed keys enter their second product
+    rounded to bf16, the way the output leaves: a term meets one of the first two and at most one of the third, each
+    off by at most UBF of it."""
     c = (dk + dv + 2 * longest + 64) * 2 * U32
-    return (c + (2 * UBF * UBF if bf16 else 0.0)) * size
+    return (c + (2 * UBF + UBF * UBF if bf16 else 0.0)) * size
 
 
 def layer_norm(x, w, b, eps):
