@@ -30,10 +30,10 @@
 //   - khat^T (lane = channel) goes to tensor memory through transposing matrix
 //     loads: two bf16 terms where the state only feeds outputs, three, exact to
 //     fp32, where the final state itself is asked for.
-// Products run in the order of their issue, which lets them share columns: khat
-// lies where O1 (D = 128; its third term in the other P) or P and O1 (D = 64) come
-// to stand, and O2 where dS stood.  At D = 128 there are two P, and q k^T of the
-// next chunk is issued ahead of P v.
+// Products run in the order of their issue, which lets them share columns: O2 lies
+// where dS stood, and khat (D = 128: its third term) where P and O1 come to stand.
+// At D = 128 khat of the next chunk is formed while P v runs, and q k^T of the next
+// chunk follows P v at once.
 #include <cuda_bf16.h>
 
 #include "decay_attn.h"
@@ -53,6 +53,17 @@ __device__ __forceinline__ void tmem_take16(uint32_t taddr, float* v) {
       "tcgen05.wait::ld.sync.aligned;"
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
       : "r"(taddr)
+      : "memory");
+}
+// The same from two places.
+__device__ __forceinline__ void tmem_take16x2(uint32_t taddr, uint32_t taddr2, float* v, float* w) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3]), "=f"(w[4]), "=f"(w[5]), "=f"(w[6]), "=f"(w[7]), "=f"(w[8]), "=f"(w[9]), "=f"(w[10]), "=f"(w[11]), "=f"(w[12]), "=f"(w[13]), "=f"(w[14]), "=f"(w[15])
+      : "r"(taddr), "r"(taddr2)
       : "memory");
 }
 // 16 lanes x 16 columns: register 2 i (2 i + 1) of thread T is lane T / 4 (+ 8), column 4 i + T % 4, the
@@ -111,12 +122,64 @@ __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.al
 template <int N>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t f2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void f2_out(uint64_t v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack2(uint64_t v) {
+  float x, y;
+  f2_out(v, x, y);
+  return pack_bf16x2(x, y);
+}
 // The next bf16 term of a pair of values: packed, and taken off the values.
-__device__ __forceinline__ uint32_t take_term(float& x, float& y) {
-  const uint32_t t = pack_bf16x2(x, y);
-  x -= __uint_as_float(t << 16);
-  y -= __uint_as_float(t & 0xFFFF0000u);
+__device__ __forceinline__ uint32_t take_term(uint64_t& v) {
+  const uint32_t t = pack2(v);
+  v = fma2(f2(__uint_as_float(t << 16), __uint_as_float(t & 0xFFFF0000u)), f2(-1.f, -1.f), v);
   return t;
+}
+
+// The products and their commit, by the one thread of a warp whose `on` is set: the warp's control flow and operands
+// stay uniform, so that the descriptors are formed in uniform registers.
+__device__ __forceinline__ void mma_ss(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "setp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "setp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t on, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
 }
 
 // Second operand read MN-major: rows are the contracted index, atoms of 64 columns `atom` bytes apart.
@@ -141,30 +204,30 @@ struct TcCfg {
   static constexpr int OFF_T = OFF_S + (STATES ? 0 : S_ATOM * (D / 64));
   // registers: 512 x 104 + 128 x 56 of 640 x 96 (D = 128), 256 x 96 + 128 x 48 of 384 x 80 (D = 64)
   static constexpr int REGS = SMALL ? 96 : 104, REGS_SERVICE = SMALL ? 48 : 56;
-  // tensor memory columns
+  // tensor memory columns (khat: 64 a term)
   static constexpr int TM_COLS = SMALL ? 256 : 512;
-  static constexpr int TM_O1 = SMALL ? 128 : 256, TM_DS = SMALL ? 192 : 384, TM_O2 = TM_DS;
+  static constexpr int TM_P = 0, TM_O1 = 128, TM_DS = SMALL ? 192 : (STATES ? 384 : 256), TM_O2 = TM_DS;
   static constexpr int PW = C / CG;               // P columns of a thread
-  // first column of P of chunk m
-  __device__ static __forceinline__ uint32_t tm_p(int m) { return SMALL ? 0 : (m & 1) * 128; }
-  // first column of term i (64 columns) of khat of chunk m
+  // first column of term i of khat of chunk m
   __device__ static __forceinline__ uint32_t tm_k(int m, int i) {
     if (SMALL) return 64 * i;
     if (STATES) return (m & 1) * 192 + 64 * i;
-    return i < 2 ? TM_O1 + 64 * i : ((m + 1) & 1) * 128;
+    return i < 2 ? 384 + 64 * i : TM_O1;
   }
 };
 
 struct TcTables {
   float pw[C + 4];                  // lambda^i
   float2 step[kSteps];              // lambda^i = hi + lo of a chunk's or segment's tokens
-  float p16[16];                    // lambda^(15-i), mirrored tiles: lambda^i
+  float pa[32];                     // a lambda^i
+  alignas(16) float p16[16];        // lambda^(15-i), mirrored tiles: lambda^i
   float wk[2][C];                   // b lambda^(n-1-s) of chunk m in m & 1, 0 past its end
   uint64_t full[2];                 // the chunk's tiles have come
   uint64_t landed[2];               // k and v of a chunk that ends inside its tiles
   uint64_t free_[3][2];             // tile x (k, v, q) of the chunk is no longer read
   uint64_t bar_k, bar_p;            // the workers': khat (with S) written, P written (and dS read)
-  uint64_t bar_qk[2], bar_ds, bar_qs, bar_pv, bar_end;  // the tensor core's
+  uint64_t bar_qk, bar_ds, bar_qs, bar_pv, bar_end;  // the tensor core's
+  DecayUnit u;
   uint32_t tmem;
   int abort;
 };
@@ -191,10 +254,10 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       mbar_init(&sh.free_[0][i], 1);
       mbar_init(&sh.free_[1][i], 1);
       mbar_init(&sh.free_[2][i], NT / 32);
-      mbar_init(&sh.bar_qk[i], 1);
     }
     mbar_init(&sh.bar_k, NT / 32);
     mbar_init(&sh.bar_p, NT / 32);
+    mbar_init(&sh.bar_qk, 1);
     mbar_init(&sh.bar_ds, 1);
     mbar_init(&sh.bar_qs, 1);
     mbar_init(&sh.bar_pv, 1);
@@ -210,26 +273,29 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   const float g = a.g[h];
   // tile row i holds scan position i of the chunk, or 127 - i where a reversed scan's tiles stay in memory order
   const bool rev = a.fetch != kFetchTokens && (p.mode & 1);
-  DecayUnit u;
-  bool on = decay_unit(a, blockIdx.x, u);
+  DecayUnit u_;
+  bool on = decay_unit(a, blockIdx.x, u_);
   if (tid < C + kSteps) {
     // threads C ..: lambda to the tokens of a whole chunk, of the last one, of either where its first token counts
     // without its decay (lag), and of a segment
-    const int last = on ? u.n - max(u.n - 1, 0) / C * C : 0;
+    const int last = on ? u_.n - max(u_.n - 1, 0) / C * C : 0;
     const int i = tid <= C ? tid : (tid == C + kLast ? last : (tid == C + kFullLag ? C - 1 : (tid == C + kLastLag ? max(last - 1, 0) : a.seg)));
     const float2 w = decay_pow(g, i);
     if (tid <= C) sh.pw[tid] = w.x;
     if (tid >= C) sh.step[tid - C] = w;
     if (tid < 16) sh.p16[rev ? tid : 15 - tid] = w.x;
+    if (tid < 32) sh.pa[tid] = p.a * w.x;
   }
-  if (STATES && on) on = u.nseg > 1 && u.i < u.nseg - 1;  // a last segment's state is formed by the output pass
+  if (STATES && on) on = u_.nseg > 1 && u_.i < u_.nseg - 1;  // a last segment's state is formed by the output pass
   if (sb & 1023u) {  // the swizzled tiles start at 1024-byte boundaries
     set_status(a.status, DIG_ERR_CUDA);
     on = false;
   }
+  if (tid == 0) sh.u = u_;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  const DecayUnit& u = sh.u;
   const uint32_t tmem = sh.tmem;
   if (!on) {
     if (warp == W0) tmem_dealloc(tmem, F::TM_COLS);
@@ -258,61 +324,63 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
    regs_down<F::REGS_SERVICE>();
    if (warp == W0) {
     // ---- the issuing warp
-    if (ln == 0) {
-      const uint32_t id_qk = idesc_bf16(128, 128), id_v = idesc_bf16(128, nv, false, true);
-      const uint64_t s_desc = mn_desc(sb + F::OFF_S, F::S_ATOM);
-      auto kstep = [&](int ks) { return (uint64_t)(((ks >> 2) * F::ATOM + (ks & 3) * 32) >> 4); };
-      auto qk = [&](int m) {
-        const uint64_t kd = sdesc_sw<128>(tile(0, m)), qd = sdesc_sw<128>(tile(2, m));
-#pragma unroll 2
-        for (int ks = 0; ks < kk; ++ks) mma_bf16(tmem + F::tm_p(m), qd + kstep(ks), kd + kstep(ks), id_qk, ks ? 1u : 0u);
-        mma_commit(&sh.bar_qk[m & 1]);
-      };
-      int done = 0;  // chunks whose q k^T is issued
-      if (!STATES && !F::SMALL && nch > 0 && wait_bar(&sh.full[0], 0)) {
-        qk(0);
-        done = 1;
+    const uint32_t one = elect_one();
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    const uint32_t id_qk = idesc_bf16(128, 128), id_v = idesc_bf16(128, nv, false, true);
+    const uint64_t s_desc = mn_desc(sb + F::OFF_S, F::S_ATOM);
+    auto kstep = [](int ks) { return (uint64_t)(((ks >> 2) * F::ATOM + (ks & 3) * 32) >> 4); };
+    auto qk = [&](int m) {
+      const uint64_t kd = sdesc_sw<128>(tile(0, m)), qd = sdesc_sw<128>(tile(2, m));
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+        if (ks < kk) mma_ss(one, tm + F::TM_P, qd + kstep(ks), kd + kstep(ks), id_qk, ks ? 1u : 0u);
+      commit(one, &sh.bar_qk);
+    };
+    constexpr bool AHEAD = !STATES && !F::SMALL;  // q k^T of a chunk follows P v of the one before
+    auto ready = [&](int m) { return __all_sync(0xFFFFFFFFu, wait_bar(&sh.full[m & 1], (m >> 1) & 1)); };
+    if (AHEAD && nch > 0 && ready(0)) qk(0);
+#pragma unroll 1
+    for (int m = 0; m < nch; ++m) {
+      const uint32_t ph = m & 1;
+      if ((!AHEAD && !ready(m)) || !__all_sync(0xFFFFFFFFu, wait_bar(&sh.bar_k, ph))) break;
+      tc_fence_after();
+      const uint64_t v0 = mn_desc(tile(1, m), F::ATOM);
+#pragma unroll 1
+      for (int i = terms - 1; i >= 0; --i) {  // the smallest terms first
+        const uint32_t ka = tm + F::tm_k(m, i);
+#pragma unroll
+        for (int ks = 0; ks < C / 16; ++ks)
+          mma_ts(one, tm + F::TM_DS, ka + 8 * ks, v0 + (uint64_t)((2048 * ks) >> 4), id_v, ks == 0 && i == terms - 1 ? 0u : 1u);
       }
-      for (int m = 0; m < nch; ++m) {
-        const uint32_t ph = m & 1;
-        if (!wait_bar(&sh.full[m & 1], (m >> 1) & 1) || !wait_bar(&sh.bar_k, ph)) break;
+      commit(one, &sh.bar_ds);
+      if (STATES) {
+        commit(one, &sh.free_[0][m & 1]);
+        commit(one, &sh.free_[1][m & 1]);
+      } else {
+        if (F::SMALL) qk(m);
+        commit(one, &sh.free_[0][m & 1]);
+        const uint64_t qd = sdesc_sw<128>(tile(2, m));
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          if (ks < kk) mma_ss(one, tm + F::TM_O1, qd + kstep(ks), s_desc + (uint64_t)((2048 * ks) >> 4), id_v, ks ? 1u : 0u);
+        commit(one, &sh.bar_qs);
+        if (!__all_sync(0xFFFFFFFFu, wait_bar(&sh.bar_p, ph))) break;
         tc_fence_after();
-        if (!STATES && !F::SMALL && done == m) qk(m), done = m + 1;
-        const uint64_t v0 = mn_desc(tile(1, m), F::ATOM);
-#pragma unroll 1
-        for (int i = terms - 1; i >= 0; --i)  // the smallest terms first
-#pragma unroll 2
+#pragma unroll
+        for (int i = 1; i >= 0; --i)  // a K-step's 16 columns: 8 of the first term, 8 of the second
+#pragma unroll
           for (int ks = 0; ks < C / 16; ++ks)
-            mma_bf16_ts(tmem + F::TM_DS, tmem + F::tm_k(m, i) + 8 * ks, v0 + (uint64_t)((2048 * ks) >> 4), id_v,
-                        ks == 0 && i == terms - 1 ? 0u : 1u);
-        mma_commit(&sh.bar_ds);
-        if (STATES) {
-          mma_commit(&sh.free_[0][m & 1]);
-          mma_commit(&sh.free_[1][m & 1]);
-        } else {
-          if (F::SMALL) qk(m);
-          mma_commit(&sh.free_[0][m & 1]);
-          const uint64_t qd = sdesc_sw<128>(tile(2, m));
-#pragma unroll 2
-          for (int ks = 0; ks < kk; ++ks)
-            mma_bf16(tmem + F::TM_O1, qd + kstep(ks), s_desc + (uint64_t)((2048 * ks) >> 4), id_v, ks ? 1u : 0u);
-          mma_commit(&sh.bar_qs);
-          if (!F::SMALL && m + 1 < nch && mbar_test_wait(&sh.full[(m + 1) & 1], ((m + 1) >> 1) & 1)) qk(m + 1), done = m + 2;
-          if (!wait_bar(&sh.bar_p, ph)) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int i = 1; i >= 0; --i)  // a K-step's 16 columns: 8 of the first term, 8 of the second
-#pragma unroll 2
-            for (int ks = 0; ks < C / 16; ++ks)
-              mma_bf16_ts(tmem + F::TM_O2, tmem + F::tm_p(m) + 16 * ks + 8 * i, v0 + (uint64_t)((2048 * ks) >> 4), id_v,
-                          i == 1 && ks == 0 ? 0u : 1u);
-          mma_commit(&sh.bar_pv);
-          mma_commit(&sh.free_[1][m & 1]);
+            mma_ts(one, tm + F::TM_O2, tm + F::TM_P + 16 * ks + 8 * i, v0 + (uint64_t)((2048 * ks) >> 4), id_v, i == 1 && ks == 0 ? 0u : 1u);
+        commit(one, &sh.bar_pv);
+        commit(one, &sh.free_[1][m & 1]);
+        if (AHEAD && m + 1 < nch) {
+          if (!ready(m + 1)) break;
+          qk(m + 1);
         }
       }
-      mma_commit(&sh.bar_end);  // no product outlives the block
-      mbar_wait(&sh.bar_end, 0, kSpinLimitNs);
     }
+    commit(one, &sh.bar_end);  // no product outlives the block
+    mbar_wait(&sh.bar_end, 0, kSpinLimitNs);
     __syncwarp();
    } else {
     // ---- the fetching warps: tile x of each chunk, in 16-byte pieces where all strides allow it, else in 8-byte ones
@@ -485,93 +553,118 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       }
     };
     if constexpr (!STATES) put_state();
-    // khat^T of chunk m -> tensor memory: the warp's 32 channels, its group's tokens
+    // khat^T of chunk m -> tensor memory: the warp's 32 channels, its group's tokens.  D = 128: the third term's place
+    // is not free yet, so it waits in registers.
+    uint32_t lo[F::SMALL || STATES ? 1 : 16];
     auto convert_k = [&](int m) {
-#pragma unroll 1
+#pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int c = 32 * (warp & 3) + 16 * half;
-        if (c >= 16 * kk) break;
-        const uint32_t kt = tile(0, m) + (c >> 6) * F::ATOM;
-        const int ch = ((c & 63) >> 3) + ((ln >> 3) & 1);
+        if (c < 16 * kk) {
+          const uint32_t kt = tile(0, m) + (c >> 6) * F::ATOM;
+          const int ch = ((c & 63) >> 3) + ((ln >> 3) & 1);
 #pragma unroll 1
-        for (int s0 = cg * F::PW; s0 < (cg + 1) * F::PW; s0 += 32) {
-          uint32_t r[8];
-          float x[16];
+          for (int s0 = cg * F::PW; s0 < (cg + 1) * F::PW; s0 += 32) {
+            uint32_t r[8];
+            uint64_t x[8];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int tok = s0 + 16 * i + ((ln >> 4) << 3) + (ln & 7);
-            ldsm_t(kt + tok * 128 + ((ch ^ (tok & 7)) << 4), r + 4 * i);
-          }
+            for (int i = 0; i < 2; ++i) {
+              const int tok = s0 + 16 * i + ((ln >> 4) << 3) + (ln & 7);
+              ldsm_t(kt + tok * 128 + ((ch ^ (tok & 7)) << 4), r + 4 * i);
+            }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 w = *reinterpret_cast<const float2*>(&sh.wk[m & 1][s0 + 8 * i + 2 * (ln & 3)]);
+            for (int i = 0; i < 8; ++i) {
+              const uint64_t w = *reinterpret_cast<const uint64_t*>(&sh.wk[m & 1][s0 + 8 * (i >> 1) + 2 * (ln & 3)]);
+              x[i] = mul2(f2(__uint_as_float(r[i] << 16), __uint_as_float(r[i] & 0xFFFF0000u)), w);
+            }
+            const uint32_t at = tmem + (static_cast<uint32_t>(c) << 16) + s0 / 2;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              x[4 * i + 2 * e] = __uint_as_float(r[2 * i + e] << 16) * w.x;
-              x[4 * i + 2 * e + 1] = __uint_as_float(r[2 * i + e] & 0xFFFF0000u) * w.y;
+            for (int i = 0; i < 8; ++i) r[i] = take_term(x[i]);
+            tmem_put_16x16(at + F::tm_k(m, 0), r);
+            if (terms == 3) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) r[i] = take_term(x[i]);
+              tmem_put_16x16(at + F::tm_k(m, 1), r);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] = pack2(x[i]);
+            if (terms == 3) {
+              if constexpr (F::SMALL || STATES) tmem_put_16x16(at + F::tm_k(m, 2), r);
+              else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) lo[8 * half + i] = r[i];
+              }
+            } else {
+              tmem_put_16x16(at + F::tm_k(m, 1), r);
             }
           }
-          const uint32_t at = tmem + (static_cast<uint32_t>(c) << 16) + s0 / 2;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) r[i] = take_term(x[2 * i], x[2 * i + 1]);
-          tmem_put_16x16(at + F::tm_k(m, 0), r);
-          if (terms == 3) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r[i] = take_term(x[2 * i], x[2 * i + 1]);
-            tmem_put_16x16(at + F::tm_k(m, 1), r);
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) r[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-          tmem_put_16x16(at + F::tm_k(m, terms - 1), r);
         }
       }
       tmem_st_wait();
+    };
+    auto put_lo = [&](int m) {
+      if constexpr (!F::SMALL && !STATES) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int c = 32 * (warp & 3) + 16 * half;
+          if (c < 16 * kk) tmem_put_16x16(tmem + (static_cast<uint32_t>(c) << 16) + cg * (F::PW / 2) + F::tm_k(m, 2), lo + 8 * half);
+        }
+        tmem_st_wait();
+      }
     };
     // S = lambda^n S + dS (columns past nv hold nothing that is read)
     auto update = [&](int n, int e) {
       if (32 * (warp & 3) < D) {
         const float2 w = sh.step[(n < C ? kLast : kFull) + (e ? kFullLag - kFull : 0)];
+        const uint64_t hi = f2(w.x, w.x), low = f2(w.y, w.y);
+        float x[32];
+        tmem_take16x2(tmem + lane + F::TM_DS + 32 * cg, tmem + lane + F::TM_DS + 32 * cg + 16, x, x + 16);
 #pragma unroll
-        for (int j = 0; j < 32; j += 16) {
-          float x[16];
-          tmem_take16(tmem + lane + F::TM_DS + 32 * cg + j, x);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) S[j + i] = fmaf(w.x, S[j + i], fmaf(w.y, S[j + i], x[i]));
+        for (int i = 0; i < 32; i += 2) {
+          const uint64_t old = f2(S[i], S[i + 1]);
+          f2_out(fma2(hi, old, fma2(low, old, f2(x[i], x[i + 1]))), S[i], S[i + 1]);
         }
       }
     };
-    // P of chunk m: masked, scaled, two bf16 terms in place (each 16 columns: 8 of the first, 8 of the second)
-    auto convert_p = [&](int m) {
+    // P: masked, scaled, two bf16 terms in place (each 16 columns: 8 of the first, 8 of the second)
+    auto convert_p = [&]() {
       const int tb = 32 * (warp & 3);
 #pragma unroll 1
       for (int b = 0; b < F::PW; b += 16) {
-        const int s0 = cg * F::PW + b;
+        const int s0 = cg * F::PW + b, blk = s0 & ~31;  // a block of 32 x 32: of later positions only, of earlier ones only, or the diagonal
         uint32_t w[16];
-        if (rev ? s0 + 15 < tb : s0 > tb + 31) {  // later positions only
+        if (blk != tb && (blk > tb) != rev) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) w[i] = 0u;
         } else {
           float x[16];
-          tmem_take16(tmem + lane + F::tm_p(m) + s0, x);
-          if (rev ? s0 >= tb + 31 : s0 + 15 <= tb) {  // earlier ones only: lambda^(t - s) = lambda^(t - s0 - 15) lambda^(15 - i)
+          tmem_take16(tmem + lane + F::TM_P + s0, x);
+          if (blk != tb) {  // lambda^(t - s) = lambda^(t - s0 - 15) lambda^(15 - i)
             const float base = p.a * sh.pw[rev ? s0 - t : t - s0 - 15];
+            const uint64_t bb = f2(base, base);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] *= base * sh.p16[i];
+            for (int i = 0; i < 16; i += 4) {
+              const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&sh.p16[i]);
+              f2_out(mul2(mul2(f2(x[i], x[i + 1]), q.x), bb), x[i], x[i + 1]);
+              f2_out(mul2(mul2(f2(x[i + 2], x[i + 3]), q.y), bb), x[i + 2], x[i + 3]);
+            }
           } else {
             const int d = t - s0;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const int k = rev ? i - d : d - i;
-              x[i] = k >= 0 ? x[i] * (p.a * sh.pw[max(k, 0)]) : 0.f;
+              const float v = x[i] * sh.pa[max(k, 0)];
+              x[i] = k >= 0 ? v : 0.f;
             }
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            w[i] = take_term(x[2 * i], x[2 * i + 1]);
-            w[8 + i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+            uint64_t v = f2(x[2 * i], x[2 * i + 1]);
+            w[i] = take_term(v);
+            w[i + 8] = pack2(v);
           }
         }
-        tmem_st16(tmem + lane + F::tm_p(m) + s0, w);
+        tmem_st16(tmem + lane + F::TM_P + s0, w);
       }
       tmem_st_wait();
     };
@@ -581,15 +674,15 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       if (jj >= nv) return;
       const int s = rev ? C - 1 - t : t;
       const float f = p.c * sh.pw[s + 1 - e];
+      const uint64_t ff = f2(f, f);
       const uint32_t st = tile(2, m) + warp * 2048;
 #pragma unroll
       for (int j = 0; j < 32; j += 16) {
         float x[16], y[16];
-        tmem_take16(tmem + lane + F::TM_O1 + jj + j, x);
-        tmem_take16(tmem + lane + F::TM_O2 + jj + j, y);
+        tmem_take16x2(tmem + lane + F::TM_O1 + jj + j, tmem + lane + F::TM_O2 + jj + j, x, y);
         uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(fmaf(f, x[2 * i], y[2 * i]), fmaf(f, x[2 * i + 1], y[2 * i + 1]));
+        for (int i = 0; i < 8; ++i) w[i] = pack2(fma2(ff, f2(x[2 * i], x[2 * i + 1]), f2(y[2 * i], y[2 * i + 1])));
         sts128(st + swz_off<64>(ln, j / 8), w[0], w[1], w[2], w[3]);
         sts128(st + swz_off<64>(ln, j / 8 + 1), w[4], w[5], w[6], w[7]);
       }
@@ -639,31 +732,43 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         for (int j = 0; j < 32; j += 4) out[(j / 4) * D] = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
       }
     } else {
+      auto full = [&](int m) { wait_bar(&sh.full[m & 1], (m >> 1) & 1); };
+      if (!F::SMALL && nch > 0) {
+        full(0);
+        convert_k(0);
+      }
+#pragma unroll 1
       for (int m = 0; m < nch; ++m) {
         const uint32_t ph = m & 1;
         const int n = min(C, u.n - m * C);
         const int e = (p.lag && u.t0 + m * C == 0) ? 1 : 0;
-        wait_bar(&sh.full[m & 1], (m >> 1) & 1);
-        // the warps of these lanes have read the last chunk's outputs, where khat comes to stand
-        if (bar_or(1 + (warp & 3), 32 * CG, timed_out || *reinterpret_cast<volatile int*>(&sh.abort))) break;
-        convert_k(m);
+        if (F::SMALL) full(m);
+        // khat (D = 128: its third term) comes over the last chunk's outputs, once the warps of these lanes have read them
+        const bool stop = timed_out || *reinterpret_cast<volatile int*>(&sh.abort);
+        if (F::SMALL || terms == 3 ? bar_or(1 + (warp & 3), 32 * CG, stop) : (bool)__any_sync(0xFFFFFFFFu, stop)) break;
+        if (F::SMALL) convert_k(m);
+        else if (terms == 3) put_lo(m);
         arrive(&sh.bar_k);
         if (!F::SMALL) {
-          wait_bar(&sh.bar_qk[m & 1], (m >> 1) & 1);
+          wait_bar(&sh.bar_qk, ph);
           tc_fence_after();
-          convert_p(m);
+          convert_p();
         }
         wait_bar(&sh.bar_ds, ph);
         tc_fence_after();
         update(n, e);  // before P v, which comes to stand in dS's place
         if (F::SMALL) {
-          wait_bar(&sh.bar_qk[m & 1], (m >> 1) & 1);
+          wait_bar(&sh.bar_qk, ph);
           tc_fence_after();
-          convert_p(m);
+          convert_p();
         }
         arrive(&sh.bar_p);
         wait_bar(&sh.bar_qs, ph);
         put_state();
+        if (!F::SMALL && m + 1 < nch) {  // while the tensor core is at P v
+          full(m + 1);
+          convert_k(m + 1);
+        }
         wait_bar(&sh.bar_pv, ph);
         tc_fence_after();
         put_out(m, e);
