@@ -233,7 +233,8 @@ struct TcTables {
 };
 
 // What a segment's block does: STATES, the segment's own contribution to the state; else its outputs.
-template <int D, bool STATES>
+// FETCH: how tiles come (one way a kernel: what an SM has to hold of its code counts).
+template <int D, bool STATES, int FETCH>
 __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) decay_tc_kernel(const __grid_constant__ DecayArgs a) {
   using F = TcCfg<D, STATES>;
   static_assert(F::OFF_T + sizeof(TcTables) <= (D == 64 ? 113 : 227) * 1024, "the blocks of an SM fit its shared memory");
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   if (!STATES && a.cu && blockIdx.x == 0 && h == 0 && blockIdx.z == 0 && warp == 0) decay_check_offsets(a);
   const float g = a.g[h];
   // tile row i holds scan position i of the chunk, or 127 - i where a reversed scan's tiles stay in memory order
-  const bool rev = a.fetch != kFetchTokens && (p.mode & 1);
+  const bool rev = FETCH != kFetchTokens && (p.mode & 1);
   DecayUnit u_;
   bool on = decay_unit(a, blockIdx.x, u_);
   if (tid < C + kSteps) {
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
             sh.wk[m & 1][32 * i + ln] = s < n ? p.b * sh.pw[n - 1 - s] : 0.f;
           }
         }
-        if (a.fetch != kFetchTokens) {
+        if constexpr (FETCH != kFetchTokens) {
           const CUtensorMap& map = a.map[x == 0 ? p.mk : (x == 1 ? p.mv : p.mq)];
           // packed: rows past the sequence's end are another's, and 0 times them need not be 0
           const bool clean = x < 2 && a.cu && n < C;
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           if (ln == 0) {
             mbar_arrive_expect_tx(bar, atoms * F::ATOM);
             const int t0 = u.t0 + m * C;
-            if (a.fetch == kFetchRows) {
+            if constexpr (FETCH == kFetchRows) {
               const int r = (rev ? u.len - t0 - C : t0) + (a.cu ? u.first : 0);
               for (int i = 0; i < atoms; ++i) tma_load_5d(dst + i * F::ATOM, map, 64 * i, h, r, a.cu ? 0 : u.b, 0, bar);
             } else {
@@ -434,8 +435,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
             __syncwarp();
             if (ln == 0) mbar_arrive(&sh.full[m & 1]);
           }
-          return;
-        }
+        } else {
         int row[4];  // of tokens ln, ln + 32, ..
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -466,6 +466,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         fence_async_smem();
         __syncwarp();
         if (ln == 0) mbar_arrive(&sh.full[m & 1]);
+        }
       };
 #pragma unroll 1
       for (int m = 0; m < nch; ++m) {
@@ -793,22 +794,33 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   if (warp == W0) tmem_dealloc(tmem, F::TM_COLS);
 }
 
-template <int D, bool STATES>
+template <int D, bool STATES, int FETCH>
 cudaError_t run(const DecayArgs& a, dim3 grid, cudaStream_t s) {
   using F = TcCfg<D, STATES>;
   constexpr int smem = F::OFF_T + sizeof(TcTables);
-  const cudaError_t e = cudaFuncSetAttribute(decay_tc_kernel<D, STATES>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = cudaFuncSetAttribute(decay_tc_kernel<D, STATES, FETCH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decay_tc_kernel<D, STATES>, grid, dim3(F::NT + 128), smem, s, a);
+  return launch_pdl(decay_tc_kernel<D, STATES, FETCH>, grid, dim3(F::NT + 128), smem, s, a);
+}
+
+template <int D, int FETCH>
+cudaError_t passes(const DecayArgs& a, dim3 grid, bool multi, cudaStream_t s) {
+  cudaError_t e;
+  if (multi && (e = run<D, true, FETCH>(a, grid, s)) != cudaSuccess) return e;
+  return run<D, false, FETCH>(a, grid, s);
 }
 
 }  // namespace
 
 cudaError_t launch_decay_tc(const DecayArgs& a, int nprob, int nseg_total, bool multi, int D, cudaStream_t s) {
   const dim3 grid(nseg_total, a.H, nprob);
-  cudaError_t e;
-  if (multi && (e = D == 64 ? run<64, true>(a, grid, s) : run<128, true>(a, grid, s)) != cudaSuccess) return e;
-  return D == 64 ? run<64, false>(a, grid, s) : run<128, false>(a, grid, s);
+  auto go = [&](auto d) {
+    constexpr int DD = decltype(d)::value;
+    return a.fetch == kFetchRows   ? passes<DD, kFetchRows>(a, grid, multi, s)
+           : a.fetch == kFetchCols ? passes<DD, kFetchCols>(a, grid, multi, s)
+                                   : passes<DD, kFetchTokens>(a, grid, multi, s);
+  };
+  return D == 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
 }
 
 }  // namespace dig
