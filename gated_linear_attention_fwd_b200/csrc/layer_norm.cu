@@ -4,9 +4,11 @@
 //   xh = (x - mean) rstd,  a = dy w,
 //   dx = rstd (a - mean(a) - xh mean(a xh)),  dw = sum_rows dy xh,  db = sum_rows dy
 // Both are memory-bound: one read of x (and dy), one write of y (dx).  A row is
-// held in the registers of TPR threads (a warp up to 1024 values, then 128 or
-// 256 threads), so the variance is the two-pass one at no extra traffic; rows
-// wider than 8192 values are re-read from cache.  All sums are fp32.  The weight
+// held in the registers of TPR threads, at most 16 values each (a warp up to 512
+// values, 512 threads up to 8192), so the variance is the two-pass one at no extra
+// traffic; rows wider than that are re-read from cache.  A thread keeps its columns
+// from row to row, so weight and bias stay in registers, and asks for the next row
+// before it reduces this one.  All sums are fp32.  The weight
 // gradients are summed per thread over the block's rows, then over the block's
 // rows of threads, and the blocks' partial rows by a second kernel, all in a
 // fixed order (no atomics: the same bits from run to run).
@@ -60,25 +62,67 @@ __device__ __forceinline__ void st_vec(T* p, const float* f) {
   }
 }
 
-// Sum over the TPR threads of a row; every thread gets it.  `red` holds two sets
-// of one float per warp for rows of several warps (TPR a multiple of 32 there),
-// used in turn so that one barrier per sum is enough.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* red, int& turn) {
+// V elements as they are in memory, and as fp32.
+template <typename T, int V>
+struct Raw {
+  uint4 u;
+  __device__ __forceinline__ void load(const T* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float* f) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      } else {
+        f[i] = __uint_as_float(w[i]);
+      }
+    }
+  }
+};
+template <typename T>
+struct Raw<T, 1> {
+  T u;
+  __device__ __forceinline__ void load(const T* p) { u = *p; }
+  __device__ __forceinline__ void zero() { u = static_cast<T>(0.f); }
+  __device__ __forceinline__ void get(float* f) const { *f = static_cast<float>(u); }
+};
+
+template <int TPR>
+constexpr int threads_of = TPR > kThreads ? TPR : kThreads;
+
+// Sums of N values over the TPR threads of a row; every thread gets them.  `red`
+// holds two sets of N floats per warp for rows of several warps, used in turn so
+// that one barrier per call is enough.
+template <int TPR, int N>
+__device__ __forceinline__ void row_sums(float* v, float* red, int& turn) {
+  constexpr int WARPS = threads_of<TPR> / 32;
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1)
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xFFFFFFFFu, v[n], m);
   if constexpr (TPR > 32) {
-    static_assert(TPR == kThreads || kThreads % TPR == 0, "whole rows per block");
     const int warp = threadIdx.x >> 5;
-    float* r = red + turn * (kThreads / 32);
+    float* r = red + turn * (WARPS * N);
     turn ^= 1;
-    if ((threadIdx.x & 31) == 0) r[warp] = v;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) r[n * WARPS + warp] = v[n];
+    }
     __syncthreads();
     const int w0 = warp / (TPR / 32) * (TPR / 32);
-    v = r[w0];
 #pragma unroll
-    for (int i = 1; i < TPR / 32; ++i) v += r[w0 + i];
+    for (int n = 0; n < N; ++n) {
+      v[n] = r[n * WARPS + w0];
+#pragma unroll
+      for (int i = 1; i < TPR / 32; ++i) v[n] += r[n * WARPS + w0 + i];
+    }
   }
+}
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* red, int& turn) {
+  row_sums<TPR, 1>(&v, red, turn);
   return v;
 }
 
@@ -95,9 +139,9 @@ struct LnArgs {
 
 // Rows in registers: NV vectors of V values per thread, TPR threads per row.
 template <typename T, typename TO, int V, int NV, int TPR>
-__global__ void __launch_bounds__(kThreads) ln_fwd_kernel(const LnArgs a) {
-  __shared__ float red[2 * kThreads / 32];
-  constexpr int RPB = kThreads / TPR;
+__global__ void __launch_bounds__(threads_of<TPR>) ln_fwd_kernel(const LnArgs a) {
+  constexpr int NT = threads_of<TPR>, RPB = NT / TPR;
+  __shared__ float red[2 * NT / 32];
   const int tr = threadIdx.x % TPR;
   int turn = 0;
   const T* x = static_cast<const T*>(a.x);
@@ -105,21 +149,35 @@ __global__ void __launch_bounds__(kThreads) ln_fwd_kernel(const LnArgs a) {
   const float inv_d = 1.f / a.D;
   griddep_wait();
   griddep_launch_dependents();
-  // every thread of a block takes the same number of steps (barriers in row_sum)
-  for (long long r0 = (long long)blockIdx.x * RPB; r0 < a.rows; r0 += (long long)gridDim.x * RPB) {
-    const long long row = r0 + threadIdx.x / TPR;
-    const bool on = row < a.rows;
-    float f[NV * V];
-    float s = 0.f;
+  Raw<T, V> next[NV];
+  auto fetch = [&](long long row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + tr) * V;
-      if (on && c < a.D) ld_vec<T, V>(x + row * a.x_stride + c, f + i * V);
-      else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) f[i * V + e] = 0.f;
-      }
+      if (row < a.rows && c < a.D) next[i].load(x + row * a.x_stride + c);
+      else next[i].zero();
     }
+  };
+  const long long step = (long long)gridDim.x * RPB;
+  long long r0 = (long long)blockIdx.x * RPB;
+  fetch(r0 + threadIdx.x / TPR);
+  float w[NV * V], b[NV * V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * TPR + tr) * V;
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[i * V + e] = 1.f, b[i * V + e] = 0.f;
+    if (a.w && c < a.D) ld_vec<float, V>(a.w + c, w + i * V);
+    if (a.b && c < a.D) ld_vec<float, V>(a.b + c, b + i * V);
+  }
+  // every thread of a block takes the same number of steps (barriers in row_sum)
+  for (; r0 < a.rows; r0 += step) {
+    const long long row = r0 + threadIdx.x / TPR;
+    float f[NV * V];
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) next[i].get(f + i * V);
+    fetch(row + step);
 #pragma unroll
     for (int i = 0; i < NV * V; ++i) s += f[i];
     const float mean = row_sum<TPR>(s, red, turn) * inv_d;
@@ -135,7 +193,7 @@ __global__ void __launch_bounds__(kThreads) ln_fwd_kernel(const LnArgs a) {
       }
     }
     const float rstd = rsqrtf(row_sum<TPR>(q, red, turn) * inv_d + a.eps);
-    if (!on) continue;
+    if (row >= a.rows) continue;
     if (tr == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -144,14 +202,10 @@ __global__ void __launch_bounds__(kThreads) ln_fwd_kernel(const LnArgs a) {
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + tr) * V;
       if (c >= a.D) continue;
-      float w[V], b[V];
+      float o[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) w[e] = 1.f, b[e] = 0.f;
-      if (a.w) ld_vec<float, V>(a.w + c, w);
-      if (a.b) ld_vec<float, V>(a.b + c, b);
-#pragma unroll
-      for (int e = 0; e < V; ++e) w[e] = fmaf(f[i * V + e] * rstd, w[e], b[e]);
-      st_vec<TO, V>(y + row * a.D + c, w);
+      for (int e = 0; e < V; ++e) o[e] = fmaf(f[i * V + e] * rstd, w[i * V + e], b[i * V + e]);
+      st_vec<TO, V>(y + row * a.D + c, o);
     }
   }
 }
@@ -199,10 +253,10 @@ struct LnBwdArgs {
 };
 
 template <typename T, typename TO, int V, int NV, int TPR>
-__global__ void __launch_bounds__(kThreads) ln_bwd_kernel(const LnBwdArgs a) {
-  __shared__ float red[2 * kThreads / 32];
+__global__ void __launch_bounds__(threads_of<TPR>) ln_bwd_kernel(const LnBwdArgs a) {
+  constexpr int NT = threads_of<TPR>, RPB = NT / TPR;
+  __shared__ float red[4 * NT / 32];
   extern __shared__ float part[];  // [RPB][D], only for RPB > 1
-  constexpr int RPB = kThreads / TPR;
   const int tr = threadIdx.x % TPR, rb = threadIdx.x / TPR;
   int turn = 0;
   const T* x = static_cast<const T*>(a.x);
@@ -214,44 +268,58 @@ __global__ void __launch_bounds__(kThreads) ln_bwd_kernel(const LnBwdArgs a) {
   for (int i = 0; i < NV * V; ++i) gw[i] = gb[i] = 0.f;
   griddep_wait();
   griddep_launch_dependents();
-  for (long long r0 = (long long)blockIdx.x * RPB; r0 < a.rows; r0 += (long long)gridDim.x * RPB) {
-    const long long row = r0 + rb;
+  Raw<T, V> nx[NV], ny[NV];
+  float nmean, nrstd;
+  auto fetch = [&](long long row) {
     const bool on = row < a.rows;
-    float xh[NV * V], g[NV * V];
-    const float mean = on ? a.mean[row] : 0.f, rstd = on ? a.rstd[row] : 0.f;
+    nmean = on ? __ldg(a.mean + row) : 0.f;
+    nrstd = on ? __ldg(a.rstd + row) : 0.f;  // 0: nothing of a row that is not there counts
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + tr) * V;
       if (on && c < a.D) {
-        ld_vec<T, V>(x + row * a.x_stride + c, xh + i * V);
-        ld_vec<T, V>(dy + row * a.D + c, g + i * V);
+        nx[i].load(x + row * a.x_stride + c);
+        ny[i].load(dy + row * a.D + c);
       } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) xh[i * V + e] = mean, g[i * V + e] = 0.f;
+        nx[i].zero();
+        ny[i].zero();
       }
     }
-    float s1 = 0.f, s2 = 0.f;
+  };
+  const long long step = (long long)gridDim.x * RPB;
+  long long r0 = (long long)blockIdx.x * RPB;
+  fetch(r0 + rb);
+  float w[NV * V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * TPR + tr) * V;
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[i * V + e] = 1.f;
+    if (a.w && c < a.D) ld_vec<float, V>(a.w + c, w + i * V);
+  }
+  for (; r0 < a.rows; r0 += step) {
+    const long long row = r0 + rb;
+    float xh[NV * V], g[NV * V];
+    const float mean = nmean, rstd = nrstd;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + tr) * V;
-      float w[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) w[e] = 1.f;
-      if (a.w && c < a.D) ld_vec<float, V>(a.w + c, w);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const int n = i * V + e;
-        xh[n] = (xh[n] - mean) * rstd;
-        gw[n] = fmaf(g[n], xh[n], gw[n]);
-        gb[n] += g[n];
-        g[n] *= w[e];
-        s1 += g[n];
-        s2 = fmaf(g[n], xh[n], s2);
-      }
+      nx[i].get(xh + i * V);
+      ny[i].get(g + i * V);
     }
-    s1 = row_sum<TPR>(s1, red, turn) * inv_d;
-    s2 = row_sum<TPR>(s2, red, turn) * inv_d;
-    if (!on) continue;
+    fetch(row + step);
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < NV * V; ++n) {  // past D both g and w g are 0
+      xh[n] = (xh[n] - mean) * rstd;
+      gw[n] = fmaf(g[n], xh[n], gw[n]);
+      gb[n] += g[n];
+      g[n] *= w[n];
+      s[0] += g[n];
+      s[1] = fmaf(g[n], xh[n], s[1]);
+    }
+    row_sums<TPR, 2>(s, red, turn);
+    const float s1 = s[0] * inv_d, s2 = s[1] * inv_d;
+    if (row >= a.rows) continue;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + tr) * V;
@@ -280,7 +348,7 @@ __global__ void __launch_bounds__(kThreads) ln_bwd_kernel(const LnBwdArgs a) {
         if (c < a.D) st_vec<float, V>(part + (size_t)rb * a.D + c, v + i * V);
       }
       __syncthreads();
-      for (int c = threadIdx.x; c < a.D; c += kThreads) {
+      for (int c = threadIdx.x; c < a.D; c += NT) {
         float s = part[c];
 #pragma unroll
         for (int r = 1; r < RPB; ++r) s += part[(size_t)r * a.D + c];
@@ -360,10 +428,15 @@ int ln_blocks(long long rows, int rpb, int cap) {
   const long long n = (rows + rpb - 1) / rpb;
   return (int)(n < 1 ? 1 : (n < cap ? n : cap));
 }
-constexpr int kFwdBlocks = 148 * 8;
+constexpr int kSms = 148;
 
-// Picks <V, NV, TPR> for D: 16-byte vectors where `vec` allows them, a warp per
-// row up to 1024 values (32 per lane), 128 threads up to 4096, 256 up to 8192.
+// Blocks of the forward on an SM: as many as run at once (a block keeps its columns' weights from row to row).
+int ln_per_sm(const void* kernel, int threads) {
+  int n = 0;
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) == cudaSuccess && n > 0 ? n : 1;
+}
+
+// Picks <V, NV, TPR> for D: 16-byte vectors where `vec` allows them, and at most 16 values per thread.
 template <typename T, typename F>
 cudaError_t ln_pick(int D, bool vec, F&& f) {
   constexpr int V = 16 / sizeof(T);
@@ -372,21 +445,22 @@ cudaError_t ln_pick(int D, bool vec, F&& f) {
     using std::integral_constant;
     if (D <= 256) return f(integral_constant<int, W>{}, integral_constant<int, 8 / W>{}, integral_constant<int, 32>{});
     if (D <= 512) return f(integral_constant<int, W>{}, integral_constant<int, 16 / W>{}, integral_constant<int, 32>{});
-    if (D <= 1024) return f(integral_constant<int, W>{}, integral_constant<int, 32 / W>{}, integral_constant<int, 32>{});
+    if (D <= 1024) return f(integral_constant<int, W>{}, integral_constant<int, 16 / W>{}, integral_constant<int, 64>{});
     if (D <= 2048) return f(integral_constant<int, W>{}, integral_constant<int, 16 / W>{}, integral_constant<int, 128>{});
-    if (D <= 4096) return f(integral_constant<int, W>{}, integral_constant<int, 32 / W>{}, integral_constant<int, 128>{});
-    return f(integral_constant<int, W>{}, integral_constant<int, 32 / W>{}, integral_constant<int, 256>{});
+    if (D <= 4096) return f(integral_constant<int, W>{}, integral_constant<int, 16 / W>{}, integral_constant<int, 256>{});
+    return f(integral_constant<int, W>{}, integral_constant<int, 16 / W>{}, integral_constant<int, 512>{});
   };
   return vec ? go(std::integral_constant<int, V>{}) : go(std::integral_constant<int, 1>{});
 }
 
 template <typename T, typename TO>
 cudaError_t ln_fwd_launch(const LnArgs& a, bool vec, cudaStream_t s) {
-  if (a.D > 8192) return launch_pdl(ln_fwd_wide_kernel<T, TO>, dim3(ln_blocks(a.rows, 1, kFwdBlocks)), dim3(kThreads), 0, s, a);
+  if (a.D > 8192) return launch_pdl(ln_fwd_wide_kernel<T, TO>, dim3(ln_blocks(a.rows, 1, 8 * kSms)), dim3(kThreads), 0, s, a);
   return ln_pick<T>(a.D, vec, [&](auto v, auto nv, auto tpr) {
-    constexpr int TPR = decltype(tpr)::value;
-    return launch_pdl(ln_fwd_kernel<T, TO, decltype(v)::value, decltype(nv)::value, TPR>,
-                      dim3(ln_blocks(a.rows, kThreads / TPR, kFwdBlocks)), dim3(kThreads), 0, s, a);
+    constexpr int TPR = decltype(tpr)::value, NT = threads_of<TPR>;
+    auto k = ln_fwd_kernel<T, TO, decltype(v)::value, decltype(nv)::value, TPR>;
+    static const int per_sm = [&] { return ln_per_sm(reinterpret_cast<const void*>(k), NT); }();
+    return launch_pdl(k, dim3(ln_blocks(a.rows, NT / TPR, kSms * per_sm)), dim3(NT), 0, s, a);
   });
 }
 
@@ -398,11 +472,11 @@ cudaError_t ln_bwd_launch(const LnBwdArgs& a, bool vec, cudaStream_t s, int* blo
     return launch_pdl(ln_bwd_wide_kernel<T, TO>, dim3(*blocks), dim3(kThreads), 0, s, a);
   }
   return ln_pick<T>(a.D, vec, [&](auto v, auto nv, auto tpr) {
-    constexpr int TPR = decltype(tpr)::value, RPB = kThreads / TPR;
-    const size_t smem = RPB > 1 ? (size_t)RPB * a.D * 4 : 0;  // at most 8 * 1024 or 2 * 4096 floats
-    *blocks = ln_blocks(a.rows, RPB, kMaxBlocks);
+    constexpr int TPR = decltype(tpr)::value, NT = threads_of<TPR>, RPB = NT / TPR;
+    const size_t smem = RPB > 1 ? (size_t)RPB * a.D * 4 : 0;  // at most 16 * 256 floats
+    *blocks = ln_blocks(a.rows, RPB, kMaxBlocks * kThreads / NT);
     auto k = ln_bwd_kernel<T, TO, decltype(v)::value, decltype(nv)::value, TPR>;
-    return launch_pdl(k, dim3(*blocks), dim3(kThreads), smem, s, a);
+    return launch_pdl(k, dim3(*blocks), dim3(NT), smem, s, a);
   });
 }
 

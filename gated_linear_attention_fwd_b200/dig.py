@@ -337,19 +337,19 @@ def _typed(t):
 
 
 def _dense(t, name, shape, dtype, dev):
-    """Address of a contiguous tensor of exactly this shape, dtype and device (None: NULL)."""
+    """Address of a contiguous tensor of exactly this shape, dtype and device index (None: NULL)."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s, got %s %s on %s%s" % (
-            name, dtype, tuple(shape), dev, t.dtype, tuple(t.shape), t.device, "" if t.is_contiguous() else ", strided"))
-    return t.data_ptr()
+    if t.is_contiguous() and t.shape == shape and t.dtype == dtype and t.get_device() == dev:
+        return t.data_ptr()
+    raise ValueError("%s must be a contiguous %s tensor of shape %s on cuda:%d, got %s %s on %s%s" % (
+        name, dtype, tuple(shape), dev, t.dtype, tuple(t.shape), t.device, "" if t.is_contiguous() else ", strided"))
 
 
 def _tokens(t, name, H, d):
-    """Rows of a [..., H, d] tensor whose H * d values are dense, and the elements between rows."""
-    if t.shape[-2:] != (H, d):
-        raise ValueError("%s must be [..., %d, %d], got %s" % (name, H, d, tuple(t.shape)))
+    """Elements between the rows of a [..., H, d] tensor, whose H * d values must be dense."""
+    if t.is_contiguous():
+        return H * d
     st = t.stride()
     if (d > 1 and st[-1] != 1) or (H > 1 and st[-2] != d):
         raise ValueError("%s: the %d x %d values of a token must be dense" % (name, H, d))
@@ -358,6 +358,8 @@ def _tokens(t, name, H, d):
 
 def _row_stride(t, name, inner, size):
     """Elements between the rows of t (all dimensions but the last `inner`), which must be one apart in every dimension."""
+    if t.is_contiguous():
+        return size
     shape, st = t.shape[:-inner], t.stride()
     step, rows = None, 1
     if t.numel() == 0:
@@ -373,29 +375,21 @@ def _row_stride(t, name, inner, size):
     return size if step is None else step
 
 
-class _On:
-    """Makes a tensor's device current where it is not (launches go to the current device)."""
-    __slots__ = ("device", "guard")
-
-    def __init__(self, t):
-        if not t.is_cuda:
-            raise ValueError("tensors must be on a CUDA device")
-        self.device, self.guard = t.device, None
-
-    def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-
-    def __exit__(self, *e):
-        if self.guard is not None:
-            self.guard.__exit__(*e)
-
-
-def _raw_stream(stream, device):
+def _call(fn, where, dev, stream, *args):
+    """fn(*args, stream) with device `dev` current (launches go to the current device), its status checked."""
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != DIG_OK:
+        _check(st, where)
 
 
 def decay_attn_workspace_bytes(B, H, L, d_k, d_v, dtype=torch.bfloat16, packed=False, backward=False) -> int:
@@ -419,7 +413,7 @@ def _decay_shape(q, k, v, o, cu_seqlens, grid_h, grid_w):
     if k.shape != q.shape or v.shape[:-1] != q.shape[:-1]:
         raise ValueError("q, k [..., H, d_k] and v [..., H, d_v] must agree: got %s, %s, %s" % (
             tuple(q.shape), tuple(k.shape), tuple(v.shape)))
-    if not q.dtype == k.dtype == v.dtype or not q.device == k.device == v.device:
+    if not q.dtype == k.dtype == v.dtype or not q.get_device() == k.get_device() == v.get_device():
         raise ValueError("q, k and v must have one dtype and device")
     if cu_seqlens is not None:
         if len(lead) != 1 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
@@ -441,21 +435,19 @@ def dig_decay_attn_fwd(q, k, v, log_decay, o, workspace, grid_h=None, grid_w=Non
     projection may be passed), or packed [rows,H,d] with cu_seqlens [B+1] int32; log_decay [H] fp32; o like v, dense;
     S0, S_final [B,H,dk,dv] fp32 or, with slots [B] int32, pools [n,H,dk,dv].  Without a grid the L tokens are a line."""
     B, H, L, dk, dv, grid_h, grid_w, qs, ks, vs = _decay_shape(q, k, v, o, cu_seqlens, grid_h, grid_w)
-    dev = q.device
+    dev = q.get_device()
     n = B
     if slots is not None:
         pool = S0 if S0 is not None else S_final
         n = pool.shape[0] if pool is not None else 0
     state = (n, H, dk, dv)
     f32 = torch.float32
-    with _On(q):
-        st = lib.dig_decay_attn_fwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _dense(log_decay, "log_decay", (H,), f32, dev),
-            float(scale), _dense(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev), _dense(S0, "S0", state, f32, dev),
-            _dense(S_final, "S_final", state, f32, dev), _dense(slots, "slots", (B,), torch.int32, dev), n,
-            _dense(o, "o", v.shape, o.dtype, dev), B, H, L, dk, dv, grid_h, grid_w, scan_mode, _typed(q), _typed(o),
-            _dense(workspace, "workspace", workspace.shape, torch.uint8, dev), workspace.numel(), _raw_stream(stream, dev))
-    _check(st, "dig_decay_attn_fwd")
+    _call(lib.dig_decay_attn_fwd, "dig_decay_attn_fwd", dev, stream,
+          q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _dense(log_decay, "log_decay", (H,), f32, dev),
+          float(scale), _dense(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev), _dense(S0, "S0", state, f32, dev),
+          _dense(S_final, "S_final", state, f32, dev), _dense(slots, "slots", (B,), torch.int32, dev), n,
+          _dense(o, "o", v.shape, o.dtype, dev), B, H, L, dk, dv, grid_h, grid_w, scan_mode, _typed(q), _typed(o),
+          _dense(workspace, "workspace", workspace.shape, torch.uint8, dev), workspace.numel())
 
 
 def dig_decay_attn_bwd(q, k, v, log_decay, dO, dq, dk, dv, workspace, grid_h=None, grid_w=None, scan_mode=0,
@@ -463,19 +455,17 @@ def dig_decay_attn_bwd(q, k, v, log_decay, dO, dq, dk, dv, workspace, grid_h=Non
     """Gradients for dig_decay_attn_fwd (see include/dig.h): dO like v, dq, dk like q and dv like v, all dense;
     S0, dS_final, dS0 [B,H,dk,dv] fp32."""
     B, H, L, d_k, d_v, grid_h, grid_w, qs, ks, vs = _decay_shape(q, k, v, dO, cu_seqlens, grid_h, grid_w)
-    dev = q.device
+    dev = q.get_device()
     state = (B, H, d_k, d_v)
     f32 = torch.float32
-    with _On(q):
-        st = lib.dig_decay_attn_bwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _dense(log_decay, "log_decay", (H,), f32, dev),
-            float(scale), _dense(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev), _dense(S0, "S0", state, f32, dev),
-            _dense(dO, "dO", v.shape, q.dtype, dev), _dense(dS_final, "dS_final", state, f32, dev),
-            _dense(dq, "dq", q.shape, dq.dtype, dev), _dense(dk, "dk", q.shape, dq.dtype, dev),
-            _dense(dv, "dv", v.shape, dq.dtype, dev), _dense(dS0, "dS0", state, f32, dev),
-            B, H, L, d_k, d_v, grid_h, grid_w, scan_mode, _typed(q), _typed(dq),
-            _dense(workspace, "workspace", workspace.shape, torch.uint8, dev), workspace.numel(), _raw_stream(stream, dev))
-    _check(st, "dig_decay_attn_bwd")
+    _call(lib.dig_decay_attn_bwd, "dig_decay_attn_bwd", dev, stream,
+          q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _dense(log_decay, "log_decay", (H,), f32, dev),
+          float(scale), _dense(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev), _dense(S0, "S0", state, f32, dev),
+          _dense(dO, "dO", v.shape, q.dtype, dev), _dense(dS_final, "dS_final", state, f32, dev),
+          _dense(dq, "dq", q.shape, dq.dtype, dev), _dense(dk, "dk", q.shape, dq.dtype, dev),
+          _dense(dv, "dv", v.shape, dq.dtype, dev), _dense(dS0, "dS0", state, f32, dev),
+          B, H, L, d_k, d_v, grid_h, grid_w, scan_mode, _typed(q), _typed(dq),
+          _dense(workspace, "workspace", workspace.shape, torch.uint8, dev), workspace.numel())
 
 
 def dig_decay_attn_step(q, k, v, log_decay, S, o, slots=None, scale=1.0, device_status=None, stream=None):
@@ -483,39 +473,33 @@ def dig_decay_attn_step(q, k, v, log_decay, S, o, slots=None, scale=1.0, device_
     state slots[b], or b); o [B,H,dv].  device_status: optional zeroed int32 [1] (see include/dig.h)."""
     B, H, dk = q.shape
     dv = v.shape[2]
-    dev = q.device
+    dev = q.get_device()
     if k.shape != q.shape or v.shape[:2] != q.shape[:2] or not q.dtype == k.dtype == v.dtype or \
-            not dev == k.device == v.device:
+            not dev == k.get_device() == v.get_device():
         raise ValueError("q, k [B, H, d_k] and v [B, H, d_v] must agree in shape, dtype and device")
     n = S.shape[0]
-    with _On(q):
-        st = lib.dig_decay_attn_step(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), _tokens(q, "q", H, dk), _tokens(k, "k", H, dk),
-            _tokens(v, "v", H, dv), _dense(log_decay, "log_decay", (H,), torch.float32, dev), scale,
-            _dense(S, "S", (n, H, dk, dv), torch.float32, dev), _dense(slots, "slots", (B,), torch.int32, dev), n,
-            _dense(o, "o", v.shape, o.dtype, dev), B, H, dk, dv, _typed(q), _typed(o),
-            _dense(device_status, "device_status", (1,), torch.int32, dev), _raw_stream(stream, dev))
-    if st != DIG_OK:
-        _check(st, "dig_decay_attn_step")
+    _call(lib.dig_decay_attn_step, "dig_decay_attn_step", dev, stream,
+          q.data_ptr(), k.data_ptr(), v.data_ptr(), _tokens(q, "q", H, dk), _tokens(k, "k", H, dk),
+          _tokens(v, "v", H, dv), _dense(log_decay, "log_decay", (H,), torch.float32, dev), scale,
+          _dense(S, "S", (n, H, dk, dv), torch.float32, dev), _dense(slots, "slots", (B,), torch.int32, dev), n,
+          _dense(o, "o", v.shape, o.dtype, dev), B, H, dk, dv, _typed(q), _typed(o),
+          _dense(device_status, "device_status", (1,), torch.int32, dev))
 
 
 def dig_layer_norm_fwd(x, y, weight=None, bias=None, eps=1e-5, mean=None, rstd=None, stream=None):
     """y = (x - mean) * rstd * weight + bias over the last dimension; x [..., D] (rows one stride apart), y dense;
     weight, bias [D] fp32; mean, rstd [rows] fp32 outputs."""
     D = x.shape[-1]
-    dev = x.device
+    dev = x.get_device()
     if x.dim() < 1 or D == 0 or (D > 1 and x.stride(-1) != 1):
         raise ValueError("x must be [..., D] with dense rows")
     rows = x.numel() // D
     f32 = torch.float32
-    with _On(x):
-        st = lib.dig_layer_norm_fwd(
-            x.data_ptr(), _row_stride(x, "x", 1, D), _dense(weight, "weight", (D,), f32, dev),
-            _dense(bias, "bias", (D,), f32, dev), eps, _dense(y, "y", x.shape, y.dtype, dev),
-            _dense(mean, "mean", (rows,), f32, dev), _dense(rstd, "rstd", (rows,), f32, dev), rows, D, _typed(x),
-            _typed(y), _raw_stream(stream, dev))
-    if st != DIG_OK:
-        _check(st, "dig_layer_norm_fwd")
+    _call(lib.dig_layer_norm_fwd, "dig_layer_norm_fwd", dev, stream,
+          x.data_ptr(), _row_stride(x, "x", 1, D), _dense(weight, "weight", (D,), f32, dev),
+          _dense(bias, "bias", (D,), f32, dev), eps, _dense(y, "y", x.shape, y.dtype, dev),
+          _dense(mean, "mean", (rows,), f32, dev), _dense(rstd, "rstd", (rows,), f32, dev), rows, D, _typed(x),
+          _typed(y))
 
 
 def new_layer_norm_workspace(rows, D, device="cuda") -> torch.Tensor:
@@ -527,21 +511,18 @@ def dig_layer_norm_bwd(x, dy, mean, rstd, dx, weight=None, dw=None, db=None, wor
     """Gradients for dig_layer_norm_fwd: x as there, dy, dx dense and like x; mean, rstd [rows] of the forward; dw, db
     [D] fp32 (either needs the workspace)."""
     D = x.shape[-1]
-    dev = x.device
+    dev = x.get_device()
     if x.dim() < 1 or D == 0 or (D > 1 and x.stride(-1) != 1):
         raise ValueError("x must be [..., D] with dense rows")
     rows = x.numel() // D
     f32 = torch.float32
-    with _On(x):
-        st = lib.dig_layer_norm_bwd(
-            x.data_ptr(), _row_stride(x, "x", 1, D), _dense(weight, "weight", (D,), f32, dev),
-            _dense(mean, "mean", (rows,), f32, dev), _dense(rstd, "rstd", (rows,), f32, dev),
-            _dense(dy, "dy", x.shape, x.dtype, dev), _dense(dx, "dx", x.shape, dx.dtype, dev),
-            _dense(dw, "dw", (D,), f32, dev), _dense(db, "db", (D,), f32, dev), rows, D, _typed(x), _typed(dx),
-            None if workspace is None else _dense(workspace, "workspace", workspace.shape, torch.uint8, dev),
-            0 if workspace is None else workspace.numel(), _raw_stream(stream, dev))
-    if st != DIG_OK:
-        _check(st, "dig_layer_norm_bwd")
+    _call(lib.dig_layer_norm_bwd, "dig_layer_norm_bwd", dev, stream,
+          x.data_ptr(), _row_stride(x, "x", 1, D), _dense(weight, "weight", (D,), f32, dev),
+          _dense(mean, "mean", (rows,), f32, dev), _dense(rstd, "rstd", (rows,), f32, dev),
+          _dense(dy, "dy", x.shape, x.dtype, dev), _dense(dx, "dx", x.shape, dx.dtype, dev),
+          _dense(dw, "dw", (D,), f32, dev), _dense(db, "db", (D,), f32, dev), rows, D, _typed(x), _typed(dx),
+          None if workspace is None else _dense(workspace, "workspace", workspace.shape, torch.uint8, dev),
+          0 if workspace is None else workspace.numel())
 
 
 def dig_read_status(workspace, stream=None) -> int:
