@@ -137,9 +137,11 @@ struct LnArgs {
   int D;
 };
 
-// Rows in registers: NV vectors of V values per thread, TPR threads per row.
+// Rows in registers: NV vectors of V values per thread, TPR threads per row.  Left to itself the compiler takes some 80
+// registers, faster than 64 with their spills (33554 x 1000 bf16: 27 against 39 us); only with 512 threads a
+// block, of which an SM would hold one, the second block wins (4096 x 8192 bf16: 30 against 38 us).
 template <typename T, typename TO, int V, int NV, int TPR>
-__global__ void __launch_bounds__(threads_of<TPR>) ln_fwd_kernel(const LnArgs a) {
+__global__ void __launch_bounds__(threads_of<TPR>, TPR == 512 && V == 8 ? 2 : 1) ln_fwd_kernel(const LnArgs a) {
   constexpr int NT = threads_of<TPR>, RPB = NT / TPR;
   __shared__ float red[2 * NT / 32];
   const int tr = threadIdx.x % TPR;
