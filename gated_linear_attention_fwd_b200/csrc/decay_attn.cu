@@ -129,16 +129,18 @@ struct MapSource {
   int d;
   long long stride;
 };
-void encode_maps(DecayArgs& a, const MapSource* t, int n, int mode) {
+void encode_maps(DecayArgs& a, const MapSource* t, int n, const MapSource* o, int no, int mode) {
   a.fetch = kFetchTokens;
   const bool rows = a.cu || mode < 2 || a.Hg == 1 || a.Wg == 1;
   if (a.L == 0 || (!rows && a.Hg % kColRun) || !tmap_available()) return;
-  for (int i = 0; i < n; ++i) {
-    if (!al16(t[i].base) || t[i].d % 8 || t[i].stride % 8) return;
-    const uint64_t st = (uint64_t)t[i].stride, L = (uint64_t)a.L;
+  for (int i = 0; i < n + no; ++i) {
+    const MapSource& m = i < n ? t[i] : o[i - n];
+    if (!al16(m.base) || m.d % 8 || m.stride % 8) return;
+    const uint64_t st = (uint64_t)m.stride, L = (uint64_t)a.L;
     const uint64_t len[2][3] = {{L, a.cu ? 1u : (uint64_t)a.B, 1}, {(uint64_t)a.Hg, (uint64_t)a.Wg, (uint64_t)a.B}};
     const uint64_t stride[2][3] = {{st, L * st, L * st}, {st * (uint64_t)a.Wg, st, L * st}};
-    if (!tmap_heads(&a.map[i], t[i].base, t[i].d, a.H, len[!rows], stride[!rows], rows ? 128 : kColRun)) return;
+    const uint32_t box = !rows ? kColRun : (i < n ? 128 : kOutRows);
+    if (!tmap_heads(i < n ? &a.map[i] : &a.omap[i - n], m.base, m.d, a.H, len[!rows], stride[!rows], box)) return;
   }
   a.fetch = rows ? kFetchRows : kFetchCols;
 }
@@ -194,7 +196,8 @@ dig_status dig_decay_attn_fwd(const void* q, const void* k, const void* v, long 
   a.p[0] = DecayProblem{q, k, v, o, q_stride, k_stride, v_stride, S0, S_final, d_k, d_v, 0, 0, scan_mode, scale, 1.f, scale, 0, 1, 2};
   if (on_tc(dtype, out_dtype)) {
     const MapSource t[3] = {{q, d_k, q_stride}, {k, d_k, k_stride}, {v, d_v, v_stride}};
-    encode_maps(a, t, 3, scan_mode);
+    const MapSource to[1] = {{o, d_v, (long long)H * d_v}};
+    encode_maps(a, t, 3, to, 1, scan_mode);
   }
   const Cut c = cut_for(B, H, L, d_k, d_v, on_tc(dtype, out_dtype), cu_seqlens != nullptr, 1);
   return launch(a, 1, c, workspace, dtype, out_dtype, static_cast<cudaStream_t>(stream));
@@ -222,7 +225,8 @@ dig_status dig_decay_attn_bwd(const void* q, const void* k, const void* v, long 
   a.p[2] = DecayProblem{v, dO, q, dk, v_stride, os, q_stride, dS_final, nullptr, d_v, d_k, 1, 1, rev, scale, scale, 1.f, 2, 3, 0};
   if (on_tc(dtype, out_dtype)) {
     const MapSource t[4] = {{q, d_k, q_stride}, {k, d_k, k_stride}, {v, d_v, v_stride}, {dO, d_v, os}};
-    encode_maps(a, t, 4, scan_mode);
+    const MapSource to[3] = {{dq, d_k, (long long)H * d_k}, {dv, d_v, os}, {dk, d_k, (long long)H * d_k}};
+    encode_maps(a, t, 4, to, 3, scan_mode);
   }
   const Cut c = cut_for(B, H, L, d_k, d_v, on_tc(dtype, out_dtype), cu_seqlens != nullptr, 3);
   return launch(a, 3, c, workspace, dtype, out_dtype, static_cast<cudaStream_t>(stream));

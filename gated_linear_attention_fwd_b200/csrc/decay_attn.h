@@ -40,9 +40,11 @@ struct DecayProblem {
 // How the tensor-core kernel fetches tiles: token by token, or by TMA from whole-row or column maps.
 enum { kFetchTokens = 0, kFetchRows = 1, kFetchCols = 2 };
 constexpr int kColRun = 16;  // tokens of a column map's box
+constexpr int kOutRows = 32;  // tokens of a row map's box of an output
 
 struct DecayArgs {
   alignas(64) CUtensorMap map[4];
+  alignas(64) CUtensorMap omap[3];  // the problems' outputs
   int fetch;
   DecayProblem p[3];
   const float* g;  // [H] log decays

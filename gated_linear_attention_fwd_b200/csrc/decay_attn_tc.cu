@@ -182,6 +182,24 @@ __device__ __forceinline__ uint32_t elect_one() {
   return r;
 }
 
+// Probes until the phase completes, another warp has given up, or the limit has passed (then sets *abort).  The flag
+// and the timer are looked at once in 32 probes: the warps that wait share their issue slots with those that work.
+__device__ __forceinline__ bool mbar_wait_or(uint64_t* bar, uint32_t parity, int* abort) {
+  uint64_t t0 = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(abort)) return false;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kSpinLimitNs) {
+      *reinterpret_cast<volatile int*>(abort) = 1;
+      return false;
+    }
+  }
+}
+
 // Second operand read MN-major: rows are the contracted index, atoms of 64 columns `atom` bytes apart.
 __device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t atom) {
   uint64_t d = sdesc_sw<128>(addr);
@@ -254,7 +272,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       mbar_init(&sh.full[i], F::PER);
       mbar_init(&sh.free_[0][i], 1);
       mbar_init(&sh.free_[1][i], 1);
-      mbar_init(&sh.free_[2][i], NT / 32);
+      mbar_init(&sh.free_[2][i], 4);
     }
     mbar_init(&sh.bar_k, NT / 32);
     mbar_init(&sh.bar_p, NT / 32);
@@ -307,17 +325,11 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   const int kk = (p.dk + 15) / 16;                // K-steps over the key channels
   const int nv = (p.dv + 15) / 16 * 16;           // columns of the products with v or S
   auto tile = [&](int x, int m) { return sb + ((m & 1) * F::PER + x) * F::TILE; };  // x: 0 k, 1 v, 2 q
-  // Waits are bounded (2^20 probes, far beyond any legitimate wait); after one gave up every other one does, nothing
-  // more is issued and the block leaves.
+  // Waits are bounded; after one gave up every other one does, nothing more is issued and the block leaves.
   bool timed_out = false;
   auto wait_bar = [&](uint64_t* bar, uint32_t parity) {
-    for (uint32_t i = 0; !timed_out && !mbar_try_wait(bar, parity); ++i) {
-      if (*reinterpret_cast<volatile int*>(&sh.abort)) return false;
-      if (i == 1u << 20) {
-        timed_out = true;
-        sh.abort = 1;
-      }
-    }
+    if (mbar_try_wait(bar, parity)) return true;
+    if (!timed_out && !mbar_wait_or(bar, parity, &sh.abort)) timed_out = true;
     return !timed_out;
   };
 
@@ -669,7 +681,55 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       }
       tmem_st_wait();
     };
-    // The warp's 32 rows x 32 columns of the output, through its 2 KB of the q tile, to whole 64-byte pieces of rows
+    // The output rows of a whole chunk: staged over the q tile, in its layout, and stored by TMA, 32 rows at a time (one
+    // thread of the warps of these lanes; it lets go of the tile later, in put_done).
+    const bool storer = warp < 4 && ln == 0;
+    auto put_tma = [&](int m, int e) {
+      const int jj = 32 * cg;
+      if (jj < nv) {
+        const float f = p.c * sh.pw[(rev ? C - 1 - t : t) + 1 - e];
+        const uint64_t ff = f2(f, f);
+        const uint32_t st = tile(2, m) + (cg >> 1) * F::ATOM;
+#pragma unroll
+        for (int j = 0; j < 32; j += 16) {
+          float x[16], y[16];
+          tmem_take16x2(tmem + lane + F::TM_O1 + jj + j, tmem + lane + F::TM_O2 + jj + j, x, y);
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = pack2(fma2(ff, f2(x[2 * i], x[2 * i + 1]), f2(y[2 * i], y[2 * i + 1])));
+          const int ch = 4 * (cg & 1) + j / 8;
+          sts128(st + swz_off<128>(t, ch), w[0], w[1], w[2], w[3]);
+          sts128(st + swz_off<128>(t, ch + 1), w[4], w[5], w[6], w[7]);
+        }
+      }
+      fence_async_smem();
+      named_bar(5 + (warp & 3), 32 * CG);
+      if (storer) {
+        const CUtensorMap& map = a.omap[blockIdx.z];
+        const uint32_t src = tile(2, m) + warp * 4096;
+        const int atoms = (p.dv + 63) / 64, t0 = u.t0 + m * C, i0 = 32 * warp;
+        if constexpr (FETCH == kFetchRows) {
+          const int r = (rev ? u.len - t0 - C : t0) + i0 + (a.cu ? u.first : 0);
+          for (int i = 0; i < atoms; ++i) tma_store_5d(map, 64 * i, h, r, a.cu ? 0 : u.b, 0, src + i * F::ATOM);
+        } else {
+          const int f0 = (rev ? a.L - t0 - C : t0) + i0;
+          int col = f0 / a.Hg, y = f0 - col * a.Hg;
+          for (int r = 0; r < 32; r += kColRun) {
+            for (int i = 0; i < atoms; ++i) tma_store_5d(map, 64 * i, h, y, col, u.b, src + i * F::ATOM + r * 128);
+            y += kColRun;
+            if (y >= a.Hg) y = 0, ++col;
+          }
+        }
+        bulk_commit();
+      }
+    };
+    // The tile that chunk m's outputs were staged in may be fetched over.
+    auto put_done = [&](int m) {
+      if (FETCH != kFetchTokens && storer) bulk_wait_read_all();
+      __syncwarp();
+      if (storer) mbar_arrive(&sh.free_[2][m & 1]);
+    };
+    // The same of any chunk: the warp's 32 rows x 32 columns through its 2 KB of the q tile, to 64-byte pieces of rows
     auto put_out = [&](int m, int e) {
       const int jj = 32 * cg;
       if (jj >= nv) return;
@@ -755,6 +815,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           tc_fence_after();
           convert_p();
         }
+        if (FETCH != kFetchTokens && m > 0) put_done(m - 1);
         wait_bar(&sh.bar_ds, ph);
         tc_fence_after();
         update(n, e);  // before P v, which comes to stand in dS's place
@@ -772,11 +833,18 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         }
         wait_bar(&sh.bar_pv, ph);
         tc_fence_after();
-        put_out(m, e);
-        fence_async_smem();  // the next tile comes over what was staged there
-        __syncwarp();
-        if (ln == 0) mbar_arrive(&sh.free_[2][m & 1]);
+        if (FETCH != kFetchTokens && n == C) {
+          put_tma(m, e);
+        } else {
+          put_out(m, e);
+          if (FETCH == kFetchTokens) {  // (elsewhere only a segment's last chunk comes here, over whose tile nothing is fetched)
+            fence_async_smem();
+            named_bar(5 + (warp & 3), 32 * CG);
+            put_done(m);
+          }
+        }
       }
+      if (FETCH != kFetchTokens && storer) bulk_wait_all();
       if (p.Sf && u.slot >= 0 && u.i == u.nseg - 1 && key) {
         // dS0 = lambda G_0; an empty sequence passes its state on as it is
         const float w = p.lag && u.len > 0 ? sh.pw[1] : 1.f;

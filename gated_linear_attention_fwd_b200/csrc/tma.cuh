@@ -92,6 +92,11 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap& m, int x, int y,
                "r"(x), "r"(y), "r"(z), "r"(w), "r"(src)
                : "memory");
 }
+__device__ __forceinline__ void tma_store_5d(const CUtensorMap& m, int x, int y, int z, int w, int v, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.5d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4, %5}], [%6];" ::"l"(tmap_addr(m)),
+               "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(src)
+               : "memory");
+}
 __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap& m, int x, int y, uint32_t src) {
   asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                    tmap_addr(m)),
