@@ -207,6 +207,10 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t atom) {
   return d | static_cast<uint64_t>((atom >> 4) & 0x3FFF) << 16;
 }
 
+// Registers: 96 for every thread at D = 128, 256 x 96 + 128 x 48 of 384 x 80 at D = 64.  What does not fit goes to local
+// memory, for which little L1 is left beside the tiles: a load from there costs a trip to L2.
+constexpr int kSmallWorkerRegs = 96, kSmallServiceRegs = 48;
+
 enum { kFull, kLast, kFullLag, kLastLag, kSegment, kSteps };
 
 template <int D, bool STATES>
@@ -220,12 +224,11 @@ struct TcCfg {
   static constexpr int S_ATOM = D * 128;
   static constexpr int OFF_S = PER * 2 * TILE;
   static constexpr int OFF_T = OFF_S + (STATES ? 0 : S_ATOM * (D / 64));
-  // registers: 512 x 104 + 128 x 56 of 640 x 96 (D = 128), 256 x 96 + 128 x 48 of 384 x 80 (D = 64)
-  static constexpr int REGS = SMALL ? 96 : 104, REGS_SERVICE = SMALL ? 48 : 56;
   // tensor memory columns (khat: 64 a term)
   static constexpr int TM_COLS = SMALL ? 256 : 512;
   static constexpr int TM_P = 0, TM_O1 = 128, TM_DS = SMALL ? 192 : (STATES ? 384 : 256), TM_O2 = TM_DS;
   static constexpr int PW = C / CG;               // P columns of a thread
+  static constexpr bool THREE_AT_ONCE = SMALL || STATES;
   // first column of term i of khat of chunk m
   __device__ static __forceinline__ uint32_t tm_k(int m, int i) {
     if (SMALL) return 64 * i;
@@ -240,7 +243,7 @@ struct TcTables {
   float pa[32];                     // a lambda^i
   alignas(16) float p16[16];        // lambda^(15-i), mirrored tiles: lambda^i
   float wk[2][C];                   // b lambda^(n-1-s) of chunk m in m & 1, 0 past its end
-  uint64_t full[2];                 // the chunk's tiles have come
+  uint64_t full[3][2];              // tile x (k, v, q) of the chunk has come
   uint64_t landed[2];               // k and v of a chunk that ends inside its tiles
   uint64_t free_[3][2];             // tile x (k, v, q) of the chunk is no longer read
   uint64_t bar_k, bar_p;            // the workers': khat (with S) written, P written (and dS read)
@@ -269,10 +272,10 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.full[i], F::PER);
-      mbar_init(&sh.free_[0][i], 1);
-      mbar_init(&sh.free_[1][i], 1);
-      mbar_init(&sh.free_[2][i], 4);
+      for (int x = 0; x < 3; ++x) {
+        mbar_init(&sh.full[x][i], 1);
+        mbar_init(&sh.free_[x][i], x == 1 && !STATES ? 4 : 1);
+      }
     }
     mbar_init(&sh.bar_k, NT / 32);
     mbar_init(&sh.bar_p, NT / 32);
@@ -334,7 +337,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   };
 
   if (warp >= W0) {
-   regs_down<F::REGS_SERVICE>();
+   if constexpr (F::SMALL) regs_down<kSmallServiceRegs>();
    if (warp == W0) {
     // ---- the issuing warp
     const uint32_t one = elect_one();
@@ -350,12 +353,12 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       commit(one, &sh.bar_qk);
     };
     constexpr bool AHEAD = !STATES && !F::SMALL;  // q k^T of a chunk follows P v of the one before
-    auto ready = [&](int m) { return __all_sync(0xFFFFFFFFu, wait_bar(&sh.full[m & 1], (m >> 1) & 1)); };
-    if (AHEAD && nch > 0 && ready(0)) qk(0);
+    auto ready = [&](int x, int m) { return __all_sync(0xFFFFFFFFu, wait_bar(&sh.full[x][m & 1], (m >> 1) & 1)); };
+    if (AHEAD && nch > 0 && ready(0, 0) && ready(2, 0)) qk(0);
 #pragma unroll 1
     for (int m = 0; m < nch; ++m) {
       const uint32_t ph = m & 1;
-      if ((!AHEAD && !ready(m)) || !__all_sync(0xFFFFFFFFu, wait_bar(&sh.bar_k, ph))) break;
+      if (!ready(1, m) || !__all_sync(0xFFFFFFFFu, wait_bar(&sh.bar_k, ph))) break;
       tc_fence_after();
       const uint64_t v0 = mn_desc(tile(1, m), F::ATOM);
 #pragma unroll 1
@@ -370,13 +373,17 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         commit(one, &sh.free_[0][m & 1]);
         commit(one, &sh.free_[1][m & 1]);
       } else {
-        if (F::SMALL) qk(m);
+        if (F::SMALL) {
+          if (!ready(2, m)) break;
+          qk(m);
+        }
         commit(one, &sh.free_[0][m & 1]);
         const uint64_t qd = sdesc_sw<128>(tile(2, m));
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
           if (ks < kk) mma_ss(one, tm + F::TM_O1, qd + kstep(ks), s_desc + (uint64_t)((2048 * ks) >> 4), id_v, ks ? 1u : 0u);
         commit(one, &sh.bar_qs);
+        commit(one, &sh.free_[2][m & 1]);
         if (!__all_sync(0xFFFFFFFFu, wait_bar(&sh.bar_p, ph))) break;
         tc_fence_after();
 #pragma unroll
@@ -385,9 +392,8 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           for (int ks = 0; ks < C / 16; ++ks)
             mma_ts(one, tm + F::TM_O2, tm + F::TM_P + 16 * ks + 8 * i, v0 + (uint64_t)((2048 * ks) >> 4), id_v, i == 1 && ks == 0 ? 0u : 1u);
         commit(one, &sh.bar_pv);
-        commit(one, &sh.free_[1][m & 1]);
         if (AHEAD && m + 1 < nch) {
-          if (!ready(m + 1)) break;
+          if (!ready(0, m + 1) || !ready(2, m + 1)) break;
           qk(m + 1);
         }
       }
@@ -418,7 +424,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           const CUtensorMap& map = a.map[x == 0 ? p.mk : (x == 1 ? p.mv : p.mq)];
           // packed: rows past the sequence's end are another's, and 0 times them need not be 0
           const bool clean = x < 2 && a.cu && n < C;
-          uint64_t* bar = clean ? &sh.landed[x] : &sh.full[m & 1];
+          uint64_t* bar = clean ? &sh.landed[x] : &sh.full[x][m & 1];
           const int atoms = min(D / 64, (d + 63) / 64);
           __syncwarp();
           if (ln == 0) {
@@ -445,7 +451,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
               for (int j = 0; j < atoms; ++j) sts128(dst + j * F::ATOM + (r0 + i / 8) * 128 + (i % 8) * 16, 0, 0, 0, 0);
             fence_async_smem();
             __syncwarp();
-            if (ln == 0) mbar_arrive(&sh.full[m & 1]);
+            if (ln == 0) mbar_arrive(&sh.full[x][m & 1]);
           }
         } else {
         int row[4];  // of tokens ln, ln + 32, ..
@@ -477,7 +483,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         cp_wait<0>();
         fence_async_smem();
         __syncwarp();
-        if (ln == 0) mbar_arrive(&sh.full[m & 1]);
+        if (ln == 0) mbar_arrive(&sh.full[x][m & 1]);
         }
       };
 #pragma unroll 1
@@ -488,7 +494,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     }
    }
   } else {
-    regs_up<F::REGS>();
+    if constexpr (F::SMALL) regs_up<kSmallWorkerRegs>();
     const int t = tid & 127, cg = tid >> 7;  // token row or key channel (the thread's TMEM lane); column group
     const uint32_t lane = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const bool key = t < D && t < p.dk;      // this lane holds a key channel of the state
@@ -566,65 +572,48 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       }
     };
     if constexpr (!STATES) put_state();
-    // khat^T of chunk m -> tensor memory: the warp's 32 channels, its group's tokens.  D = 128: the third term's place
-    // is not free yet, so it waits in registers.
-    uint32_t lo[F::SMALL || STATES ? 1 : 16];
-    auto convert_k = [&](int m) {
-#pragma unroll
+    // khat^T of chunk m -> tensor memory: the warp's 32 channels, its group's tokens.  LAST: the last of three terms alone,
+    // formed again once its place is free (held in registers meanwhile it would push others out to local memory).
+    auto convert_k = [&](int m, auto last) {
+      constexpr bool LAST = decltype(last)::value;
+#pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         const int c = 32 * (warp & 3) + 16 * half;
-        if (c < 16 * kk) {
-          const uint32_t kt = tile(0, m) + (c >> 6) * F::ATOM;
-          const int ch = ((c & 63) >> 3) + ((ln >> 3) & 1);
+        if (c >= 16 * kk) break;
+        const uint32_t kt = tile(0, m) + (c >> 6) * F::ATOM;
+        const int ch = ((c & 63) >> 3) + ((ln >> 3) & 1);
 #pragma unroll 1
-          for (int s0 = cg * F::PW; s0 < (cg + 1) * F::PW; s0 += 32) {
-            uint32_t r[8];
-            uint64_t x[8];
+        for (int s0 = cg * F::PW; s0 < (cg + 1) * F::PW; s0 += 32) {
+          uint32_t r[8];
+          uint64_t x[8];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int tok = s0 + 16 * i + ((ln >> 4) << 3) + (ln & 7);
-              ldsm_t(kt + tok * 128 + ((ch ^ (tok & 7)) << 4), r + 4 * i);
-            }
+          for (int i = 0; i < 2; ++i) {
+            const int tok = s0 + 16 * i + ((ln >> 4) << 3) + (ln & 7);
+            ldsm_t(kt + tok * 128 + ((ch ^ (tok & 7)) << 4), r + 4 * i);
+          }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint64_t w = *reinterpret_cast<const uint64_t*>(&sh.wk[m & 1][s0 + 8 * (i >> 1) + 2 * (ln & 3)]);
-              x[i] = mul2(f2(__uint_as_float(r[i] << 16), __uint_as_float(r[i] & 0xFFFF0000u)), w);
-            }
-            const uint32_t at = tmem + (static_cast<uint32_t>(c) << 16) + s0 / 2;
+          for (int i = 0; i < 8; ++i) {
+            const uint64_t w = *reinterpret_cast<const uint64_t*>(&sh.wk[m & 1][s0 + 8 * (i >> 1) + 2 * (ln & 3)]);
+            x[i] = mul2(f2(__uint_as_float(r[i] << 16), __uint_as_float(r[i] & 0xFFFF0000u)), w);
+          }
+          const uint32_t at = tmem + (static_cast<uint32_t>(c) << 16) + s0 / 2;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) r[i] = take_term(x[i]);
+          if (!LAST) tmem_put_16x16(at + F::tm_k(m, 0), r);
+          if (LAST || (F::THREE_AT_ONCE && terms == 3)) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) r[i] = take_term(x[i]);
-            tmem_put_16x16(at + F::tm_k(m, 0), r);
-            if (terms == 3) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) r[i] = take_term(x[i]);
-              tmem_put_16x16(at + F::tm_k(m, 1), r);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r[i] = pack2(x[i]);
-            if (terms == 3) {
-              if constexpr (F::SMALL || STATES) tmem_put_16x16(at + F::tm_k(m, 2), r);
-              else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) lo[8 * half + i] = r[i];
-              }
-            } else {
-              tmem_put_16x16(at + F::tm_k(m, 1), r);
-            }
+            if (!LAST) tmem_put_16x16(at + F::tm_k(m, 1), r);
           }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) r[i] = pack2(x[i]);
+          tmem_put_16x16(at + F::tm_k(m, LAST || (F::THREE_AT_ONCE && terms == 3) ? 2 : 1), r);
         }
       }
       tmem_st_wait();
     };
-    auto put_lo = [&](int m) {
-      if constexpr (!F::SMALL && !STATES) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int c = 32 * (warp & 3) + 16 * half;
-          if (c < 16 * kk) tmem_put_16x16(tmem + (static_cast<uint32_t>(c) << 16) + cg * (F::PW / 2) + F::tm_k(m, 2), lo + 8 * half);
-        }
-        tmem_st_wait();
-      }
-    };
+    constexpr std::integral_constant<bool, false> kAll{};
+    constexpr std::integral_constant<bool, true> kThird{};
     // S = lambda^n S + dS (columns past nv hold nothing that is read)
     auto update = [&](int n, int e) {
       if (32 * (warp & 3) < D) {
@@ -681,7 +670,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       }
       tmem_st_wait();
     };
-    // The output rows of a whole chunk: staged over the q tile, in its layout, and stored by TMA, 32 rows at a time (one
+    // The output rows of a whole chunk: staged over the v tile, in its layout, and stored by TMA, 32 rows at a time (one
     // thread of the warps of these lanes; it lets go of the tile later, in put_done).
     const bool storer = warp < 4 && ln == 0;
     auto put_tma = [&](int m, int e) {
@@ -689,7 +678,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       if (jj < nv) {
         const float f = p.c * sh.pw[(rev ? C - 1 - t : t) + 1 - e];
         const uint64_t ff = f2(f, f);
-        const uint32_t st = tile(2, m) + (cg >> 1) * F::ATOM;
+        const uint32_t st = tile(1, m) + (cg >> 1) * F::ATOM;
 #pragma unroll
         for (int j = 0; j < 32; j += 16) {
           float x[16], y[16];
@@ -706,7 +695,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       named_bar(5 + (warp & 3), 32 * CG);
       if (storer) {
         const CUtensorMap& map = a.omap[blockIdx.z];
-        const uint32_t src = tile(2, m) + warp * 4096;
+        const uint32_t src = tile(1, m) + warp * 4096;
         const int atoms = (p.dv + 63) / 64, t0 = u.t0 + m * C, i0 = 32 * warp;
         if constexpr (FETCH == kFetchRows) {
           const int r = (rev ? u.len - t0 - C : t0) + i0 + (a.cu ? u.first : 0);
@@ -727,16 +716,16 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     auto put_done = [&](int m) {
       if (FETCH != kFetchTokens && storer) bulk_wait_read_all();
       __syncwarp();
-      if (storer) mbar_arrive(&sh.free_[2][m & 1]);
+      if (storer) mbar_arrive(&sh.free_[1][m & 1]);
     };
-    // The same of any chunk: the warp's 32 rows x 32 columns through its 2 KB of the q tile, to 64-byte pieces of rows
+    // The same of any chunk: the warp's 32 rows x 32 columns through its 2 KB of the v tile, to 64-byte pieces of rows
     auto put_out = [&](int m, int e) {
       const int jj = 32 * cg;
       if (jj >= nv) return;
       const int s = rev ? C - 1 - t : t;
       const float f = p.c * sh.pw[s + 1 - e];
       const uint64_t ff = f2(f, f);
-      const uint32_t st = tile(2, m) + warp * 2048;
+      const uint32_t st = tile(1, m) + warp * 2048;
 #pragma unroll
       for (int j = 0; j < 32; j += 16) {
         float x[16], y[16];
@@ -774,9 +763,9 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       constexpr bool AHEAD = !F::SMALL;
       for (int m = 0; m < nch + (AHEAD ? 1 : 0); ++m) {
         if (m < nch) {
-          wait_bar(&sh.full[m & 1], (m >> 1) & 1);
+          wait_bar(&sh.full[0][m & 1], (m >> 1) & 1);
           if (__any_sync(0xFFFFFFFFu, timed_out || *reinterpret_cast<volatile int*>(&sh.abort))) break;
-          convert_k(m);
+          convert_k(m, kAll);
         }
         const int j = AHEAD ? m - 1 : m;
         if (!AHEAD) arrive(&sh.bar_k);
@@ -793,10 +782,10 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         for (int j = 0; j < 32; j += 4) out[(j / 4) * D] = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
       }
     } else {
-      auto full = [&](int m) { wait_bar(&sh.full[m & 1], (m >> 1) & 1); };
+      auto full = [&](int m) { wait_bar(&sh.full[0][m & 1], (m >> 1) & 1); };
       if (!F::SMALL && nch > 0) {
         full(0);
-        convert_k(0);
+        convert_k(0, kAll);
       }
 #pragma unroll 1
       for (int m = 0; m < nch; ++m) {
@@ -807,8 +796,8 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         // khat (D = 128: its third term) comes over the last chunk's outputs, once the warps of these lanes have read them
         const bool stop = timed_out || *reinterpret_cast<volatile int*>(&sh.abort);
         if (F::SMALL || terms == 3 ? bar_or(1 + (warp & 3), 32 * CG, stop) : (bool)__any_sync(0xFFFFFFFFu, stop)) break;
-        if (F::SMALL) convert_k(m);
-        else if (terms == 3) put_lo(m);
+        if (F::SMALL) convert_k(m, kAll);
+        else if (terms == 3) convert_k(m, kThird);
         arrive(&sh.bar_k);
         if (!F::SMALL) {
           wait_bar(&sh.bar_qk, ph);
@@ -829,7 +818,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         put_state();
         if (!F::SMALL && m + 1 < nch) {  // while the tensor core is at P v
           full(m + 1);
-          convert_k(m + 1);
+          convert_k(m + 1, kAll);
         }
         wait_bar(&sh.bar_pv, ph);
         tc_fence_after();
