@@ -11,7 +11,6 @@
 namespace dig {
 
 void set_last_error(const char* msg);       // dig_api.cu
-unsigned long long spin_limit_ns();         // dig_api.cu
 
 namespace {
 
@@ -87,10 +86,44 @@ bool size_ok(int B, int H, int L, int d_k, int d_v, bool packed) {
 // bf16 in and out runs on the tensor core (chunks of 128 tokens), the rest on the FP32 pipes (chunks of 32).
 bool on_tc(int dtype, int out_dtype) { return dtype == DIG_BF16 && out_dtype == DIG_BF16; }
 
-Cut cut_for(int B, int H, int L, int dk, int dv, bool tc, bool packed, int nprob) {
-  const bool small = dk <= 64 && dv <= 64;
-  return tc ? cut_of(B, H, L, dk, dv, 128, small ? 2 : 1, packed, nprob)
-            : cut_of(B, H, L, dk, dv, 32, small ? 3 : 1, packed, nprob);
+Cut cut_for(int B, int H, int L, int dk, int dv, bool packed, int nprob) {
+  return cut_of(B, H, L, dk, dv, 32, dk <= 64 && dv <= 64 ? 3 : 1, packed, nprob);
+}
+
+// How the tensor-core kernel's chunks are dealt.  Uncut units need one pass; cut ones fill the GPU evenly, at the price
+// of a first pass over the cut parts' k and v (0.42 of the second's time a chunk: it reads half as much), its launch,
+// and joining the earlier blocks' states (a tenth of a chunk's time each, at 128 x 128).  Packed sequences, whose
+// lengths the host does not know, are taken to be alike.
+struct Deal {
+  DecayDeal d;
+  int D;
+  bool multi;     // whether a unit may be cut
+  size_t states;  // floats
+};
+Deal deal_for(int B, int H, int L, int dk, int dv, bool packed, int nprob) {
+  Deal r{};
+  r.D = dk <= 64 && dv <= 64 ? 64 : 128;
+  const long long slots = (long long)kSms * (r.D == 64 ? 2 : 1);
+  const long long units = (long long)B * H * nprob;
+  const int n = packed ? (int)(((long long)L / 128 + B) / (B > 0 ? B : 1)) : (L > 128 ? (L + 127) / 128 : 1);
+  const long long total = units * (n > 0 ? n : 1);
+  r.d = DecayDeal{(int)(units < slots ? units : slots), n, n, nprob};
+  const bool cuttable = packed ? L > 128 : n > 1;
+  double best = packed && cuttable ? 1e30 : (double)((units + r.d.grid - 1) / r.d.grid) * n;  // packed: dealt by the chunk
+  if (cuttable) {
+    for (long long c = (total + slots - 1) / slots, k = 0; c <= n && k < 64; ++c, ++k) {
+      const double cost = c + 0.42 * (c < n ? c : n - 1) + 2.0 + 0.1 * ((n + c - 1) / c);
+      if (cost < best) {
+        best = cost;
+        r.d.grid = (int)((total + c - 1) / c);
+        r.d.gran = 1;
+      }
+    }
+  }
+  if (packed) r.d.gran = 1;
+  r.multi = cuttable && r.d.gran == 1;
+  r.states = r.multi ? (size_t)2 * r.d.grid * r.D * r.D : 0;
+  return r;
 }
 
 // The checks that the forward and the backward share.
@@ -145,15 +178,21 @@ void encode_maps(DecayArgs& a, const MapSource* t, int n, const MapSource* o, in
   a.fetch = rows ? kFetchRows : kFetchCols;
 }
 
-dig_status launch(DecayArgs& a, int nprob, const Cut& c, void* ws, int dtype, int out_dtype, cudaStream_t s) {
-  a.seg = c.seg;
-  a.nps = c.nps;
+dig_status launch(DecayArgs& a, int nprob, int dk, int dv, void* ws, int dtype, int out_dtype, cudaStream_t s) {
   a.segst = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sizeof(WsHeader));
-  a.segst_problem = (long long)c.total * a.H * c.D * c.D;
   a.status = &static_cast<WsHeader*>(ws)->status;
-  a.spin_ns = spin_limit_ns();
-  const cudaError_t e = on_tc(dtype, out_dtype) ? launch_decay_tc(a, nprob, c.total, c.multi, c.D, s)
-                                                : launch_decay_f32(a, nprob, c.total, c.multi, c.D, dtype, out_dtype, s);
+  cudaError_t e;
+  if (on_tc(dtype, out_dtype)) {
+    const Deal d = deal_for(a.B, a.H, a.L, dk, dv, a.cu != nullptr, nprob);
+    a.deal = d.d;
+    e = launch_decay_tc(a, d.multi, d.D, s);
+  } else {
+    const Cut c = cut_for(a.B, a.H, a.L, dk, dv, a.cu != nullptr, nprob);
+    a.seg = c.seg;
+    a.nps = c.nps;
+    a.segst_problem = (long long)c.total * a.H * c.D * c.D;
+    e = launch_decay_f32(a, nprob, c.total, c.multi, c.D, dtype, out_dtype, s);
+  }
   return e == cudaSuccess ? DIG_OK : attn_fail(DIG_ERR_CUDA, cudaGetErrorString(e));
 }
 
@@ -168,9 +207,9 @@ size_t dig_decay_attn_workspace_bytes(int B, int H, int L, int d_k, int d_v, int
   if (B < 0 || H <= 0 || L < 0 || d_k <= 0 || d_v <= 0 || d_k > 128 || d_v > 128 || d_k % 4 || d_v % 4 ||
       (pass != 0 && pass != 1) || (dtype != DIG_F32 && dtype != DIG_BF16) || !size_ok(B, H, L, d_k, d_v, packed != 0))
     return 0;
-  size_t n = cut_for(B, H, L, d_k, d_v, false, packed != 0, pass ? 3 : 1).states;
+  size_t n = cut_for(B, H, L, d_k, d_v, packed != 0, pass ? 3 : 1).states;
   if (dtype == DIG_BF16) {  // either output type
-    const size_t m = cut_for(B, H, L, d_k, d_v, true, packed != 0, pass ? 3 : 1).states;
+    const size_t m = deal_for(B, H, L, d_k, d_v, packed != 0, pass ? 3 : 1).states;
     n = m > n ? m : n;
   }
   return sizeof(WsHeader) + n * sizeof(float);
@@ -199,8 +238,7 @@ dig_status dig_decay_attn_fwd(const void* q, const void* k, const void* v, long 
     const MapSource to[1] = {{o, d_v, (long long)H * d_v}};
     encode_maps(a, t, 3, to, 1, scan_mode);
   }
-  const Cut c = cut_for(B, H, L, d_k, d_v, on_tc(dtype, out_dtype), cu_seqlens != nullptr, 1);
-  return launch(a, 1, c, workspace, dtype, out_dtype, static_cast<cudaStream_t>(stream));
+  return launch(a, 1, d_k, d_v, workspace, dtype, out_dtype, static_cast<cudaStream_t>(stream));
 }
 
 dig_status dig_decay_attn_bwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
@@ -228,8 +266,7 @@ dig_status dig_decay_attn_bwd(const void* q, const void* k, const void* v, long 
     const MapSource to[3] = {{dq, d_k, (long long)H * d_k}, {dv, d_v, os}, {dk, d_k, (long long)H * d_k}};
     encode_maps(a, t, 4, to, 3, scan_mode);
   }
-  const Cut c = cut_for(B, H, L, d_k, d_v, on_tc(dtype, out_dtype), cu_seqlens != nullptr, 3);
-  return launch(a, 3, c, workspace, dtype, out_dtype, static_cast<cudaStream_t>(stream));
+  return launch(a, 3, d_k, d_v, workspace, dtype, out_dtype, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

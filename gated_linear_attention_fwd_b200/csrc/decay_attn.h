@@ -37,6 +37,16 @@ struct DecayProblem {
   int mq, mk, mv;  // the tensors' maps in DecayArgs::map
 };
 
+// The tensor-core kernel's share of a call.  Every sequence, for every problem and head, is a unit of at least one
+// chunk of 128 tokens; the chunks of all units in a row are dealt to the blocks in equal runs, so a block walks the end
+// of a unit, whole units, and the beginning of one.  `gran` chunks are never parted (1, or all of a unit).
+struct DecayDeal {
+  int grid;     // blocks
+  int gran;
+  int chunks;   // of a unit (without cu)
+  int nprob;
+};
+
 // How the tensor-core kernel fetches tiles: token by token, or by TMA from whole-row or column maps.
 enum { kFetchTokens = 0, kFetchRows = 1, kFetchCols = 2 };
 constexpr int kColRun = 16;  // tokens of a column map's box
@@ -54,10 +64,10 @@ struct DecayArgs {
   int B, H, L, Hg, Wg;
   int seg;        // tokens of a segment
   int nps;        // segments of a sequence of L tokens (without cu)
-  float* segst;   // [problem][segment][H][D * D] segment states
+  DecayDeal deal;
+  float* segst;   // tensor core: [2][block][D * D], a block's unfinished unit's state and the copy of its S0; else [problem][segment][H][D * D] segment states
   long long segst_problem;  // elements between problems there
   uint32_t* status;
-  unsigned long long spin_ns;
 };
 
 struct DecayUnit {
@@ -68,7 +78,8 @@ struct DecayUnit {
 };
 
 // Row of scan position t of unit u's sequence.
-__device__ __forceinline__ int decay_row(const DecayArgs& a, const DecayUnit& u, int mode, int t) {
+template <typename U>
+__device__ __forceinline__ int decay_row(const DecayArgs& a, const U& u, int mode, int t) {
   if (a.cu) return u.first + ((mode & 1) ? u.len - 1 - t : t);
   return u.first + scan_to_grid(t, a.L, a.Hg, a.Wg, mode);
 }
@@ -77,6 +88,19 @@ __device__ __forceinline__ int decay_row(const DecayArgs& a, const DecayUnit& u,
 __device__ __forceinline__ void decay_bounds(const DecayArgs& a, int b, int& lo, int& hi) {
   lo = min(max(a.cu[b], 0), a.L);
   hi = min(max(a.cu[b + 1], lo), a.L);
+}
+
+// The state slot of sequence b, -1: none (reported where the caller asked for one); one warp.
+__device__ __forceinline__ int decay_slot(const DecayArgs& a, int b) {
+  if (!a.slots) return b;
+  int slot = a.slots[b];
+  bool bad = slot >= a.n_slots;
+  for (int j = threadIdx.x & 31; j < b && slot >= 0; j += 32) bad |= a.slots[j] == slot;
+  if (__any_sync(0xFFFFFFFFu, bad)) {
+    slot = -1;
+    if ((threadIdx.x & 31) == 0) set_status(a.status, DIG_ERR_INVALID_ARGUMENT);
+  }
+  return slot;
 }
 
 // The unit of segment slot `sidx` of the call; every lane of the calling warp
@@ -120,17 +144,85 @@ __device__ __forceinline__ bool decay_unit(const DecayArgs& a, int sidx, DecayUn
   }
   u.t0 = u.i * a.seg;
   u.n = min(a.seg, u.len - u.t0);
-  u.slot = u.b;
-  if (a.slots) {
-    u.slot = a.slots[u.b];
-    bool bad = u.slot >= a.n_slots;
-    for (int j = lane; j < u.b && u.slot >= 0; j += 32) bad |= a.slots[j] == u.slot;
-    if (__any_sync(0xFFFFFFFFu, bad)) {
-      u.slot = -1;
-      if (lane == 0) set_status(a.status, DIG_ERR_INVALID_ARGUMENT);
+  u.slot = decay_slot(a, u.b);
+  return true;
+}
+
+// Chunks of 128 tokens that a sequence of n tokens counts for (an empty one has a state to pass on).
+__device__ __forceinline__ int deal_chunks(int n) { return n > 128 ? (n + 127) / 128 : 1; }
+
+// Chunks of all sequences of a packed call (one warp).
+__device__ __forceinline__ long long deal_total(const DecayArgs& a) {
+  long long s = 0;
+  for (int b = threadIdx.x & 31; b < a.B; b += 32) {
+    int lo, hi;
+    decay_bounds(a, b, lo, hi);
+    s += deal_chunks(hi - lo);
+  }
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
+  return s;
+}
+
+// A block's walk through part of a unit.
+struct DecayPiece {
+  int b, h, z;           // sequence, head, problem
+  int first, len;        // the sequence's first row and length
+  int t0, n;             // the piece's first scan position and its tokens
+  int chunks;            // of the piece
+  bool last;             // whether the unit ends with it
+  int slot;              // state of the sequence, -1: none
+  long long unit_start;  // the unit's first chunk among all units'
+};
+
+// The piece that starts at chunk r of all units', `per` of each (problem, head), and ends before chunk r1; one warp.
+__device__ __forceinline__ void decay_piece(const DecayArgs& a, long long per, long long r, long long r1, DecayPiece& u) {
+  const int lane = threadIdx.x & 31;
+  const long long zh = r / per;
+  const long long w = r - zh * per;
+  u.h = (int)(zh % a.H);
+  u.z = (int)(zh / a.H);
+  int nch, c0;
+  if (!a.cu) {
+    nch = a.deal.chunks;
+    u.b = (int)(w / nch);
+    c0 = (int)(w - (long long)u.b * nch);
+    u.first = u.b * a.L;
+    u.len = a.L;
+  } else {
+    long long base = 0;
+    nch = 1, c0 = 0, u.b = 0, u.first = 0, u.len = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      int lo = 0, hi = 0, ns = 0;
+      if (b0 + lane < a.B) {
+        decay_bounds(a, b0 + lane, lo, hi);
+        ns = deal_chunks(hi - lo);
+      }
+      int inc = ns;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, inc, m);
+        if (lane >= m) inc += x;
+      }
+      const unsigned has = __ballot_sync(0xFFFFFFFFu, base + inc > w);
+      if (has) {
+        const int src = __ffs(has) - 1;
+        u.b = b0 + src;
+        nch = __shfl_sync(0xFFFFFFFFu, ns, src);
+        c0 = (int)(w - (base + __shfl_sync(0xFFFFFFFFu, inc, src) - nch));
+        u.first = __shfl_sync(0xFFFFFFFFu, lo, src);
+        u.len = __shfl_sync(0xFFFFFFFFu, hi, src) - u.first;
+        break;
+      }
+      base += __shfl_sync(0xFFFFFFFFu, inc, 31);
     }
   }
-  return true;
+  u.chunks = (int)min((long long)(nch - c0), r1 - r);
+  u.last = c0 + u.chunks == nch;
+  u.t0 = 128 * c0;
+  u.n = max(min(u.len - u.t0, 128 * u.chunks), 0);
+  u.unit_start = r - c0;
+  u.slot = decay_slot(a, u.b);
 }
 
 // Reports offsets that do not ascend within 0 .. L (one warp of the call does this).
@@ -149,6 +241,6 @@ __device__ __forceinline__ float2 decay_pow(float g, long long i) {
 // Launches of the two passes (states: only where a sequence has more than one segment).
 cudaError_t launch_decay_f32(const DecayArgs& a, int nprob, int nseg_total, bool multi, int D, int dtype, int out_dtype,
                              cudaStream_t s);
-cudaError_t launch_decay_tc(const DecayArgs& a, int nprob, int nseg_total, bool multi, int D, cudaStream_t s);
+cudaError_t launch_decay_tc(const DecayArgs& a, bool multi, int D, cudaStream_t s);
 
 }  // namespace dig

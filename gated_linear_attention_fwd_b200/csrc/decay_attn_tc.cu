@@ -29,7 +29,8 @@
 //     cut a little off it at every addition;
 //   - khat^T (lane = channel) goes to tensor memory through transposing matrix
 //     loads: two bf16 terms where the state only feeds outputs, three, exact to
-//     fp32, where the final state itself is asked for.
+//     fp32, where the final state itself is asked for and the chunk's part of it has
+//     not decayed below 2^-10 by then (two terms leave 2^-17 of that).
 // Products run in the order of their issue, which lets them share columns: O2 lies
 // where dS stood, and khat (D = 128: its third term) where P and O1 come to stand.
 // At D = 128 khat of the next chunk is formed while P v runs, and q k^T of the next
@@ -207,11 +208,7 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t atom) {
   return d | static_cast<uint64_t>((atom >> 4) & 0x3FFF) << 16;
 }
 
-// Registers: 96 for every thread at D = 128, 256 x 96 + 128 x 48 of 384 x 80 at D = 64.  What does not fit goes to local
-// memory, for which little L1 is left beside the tiles: a load from there costs a trip to L2.
-constexpr int kSmallWorkerRegs = 96, kSmallServiceRegs = 48;
-
-enum { kFull, kLast, kFullLag, kLastLag, kSegment, kSteps };
+enum { kFull, kLast, kFullLag, kLastLag, kRun, kRun1, kSteps };
 
 template <int D, bool STATES>
 struct TcCfg {
@@ -224,6 +221,9 @@ struct TcCfg {
   static constexpr int S_ATOM = D * 128;
   static constexpr int OFF_S = PER * 2 * TILE;
   static constexpr int OFF_T = OFF_S + (STATES ? 0 : S_ATOM * (D / 64));
+  // Registers: 512 x 104 + 128 x 56 of 640 x 96 (D = 128), 256 x 96 + 128 x 48 of 384 x 80 (D = 64).  What does not fit goes
+  // to local memory, for which little L1 is left beside the tiles: a load from there costs a trip to L2.
+  static constexpr int WORKER_REGS = SMALL ? 96 : 104, SERVICE_REGS = SMALL ? 48 : 56;
   // tensor memory columns (khat: 64 a term)
   static constexpr int TM_COLS = SMALL ? 256 : 512;
   static constexpr int TM_P = 0, TM_O1 = 128, TM_DS = SMALL ? 192 : (STATES ? 384 : 256), TM_O2 = TM_DS;
@@ -239,7 +239,7 @@ struct TcCfg {
 
 struct TcTables {
   float pw[C + 4];                  // lambda^i
-  float2 step[kSteps];              // lambda^i = hi + lo of a chunk's or segment's tokens
+  float2 step[kSteps];              // lambda^i = hi + lo of a chunk's or a block's run of tokens
   float pa[32];                     // a lambda^i
   alignas(16) float p16[16];        // lambda^(15-i), mirrored tiles: lambda^i
   float wk[2][C];                   // b lambda^(n-1-s) of chunk m in m & 1, 0 past its end
@@ -248,12 +248,17 @@ struct TcTables {
   uint64_t free_[3][2];             // tile x (k, v, q) of the chunk is no longer read
   uint64_t bar_k, bar_p;            // the workers': khat (with S) written, P written (and dS read)
   uint64_t bar_qk, bar_ds, bar_qs, bar_pv, bar_end;  // the tensor core's
-  DecayUnit u;
+  DecayPiece u;
+  float g;    // the head's log decay
+  int keep;   // whether the unit's final state is asked for
+  // how the chunks are dealt, and what of this block's run is left (kept here: registers are short)
+  long long per, grains, at, end;
+  int grid, more;
   uint32_t tmem;
   int abort;
 };
 
-// What a segment's block does: STATES, the segment's own contribution to the state; else its outputs.
+// STATES: what a block's unfinished unit adds to its state; else a block's outputs, piece by piece.
 // FETCH: how tiles come (one way a kernel: what an SM has to hold of its code counts).
 template <int D, bool STATES, int FETCH>
 __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) decay_tc_kernel(const __grid_constant__ DecayArgs a) {
@@ -263,8 +268,6 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   extern __shared__ __align__(1024) uint8_t smem[];
   TcTables& sh = *reinterpret_cast<TcTables*>(smem + F::OFF_T);
   const int tid = threadIdx.x, warp = tid >> 5, ln = tid & 31;
-  const int h = blockIdx.y;
-  const DecayProblem& p = a.p[blockIdx.z];
   const uint32_t sb = smem_u32(smem);
   if (warp == W0) {
     tmem_alloc(&sh.tmem, F::TM_COLS);
@@ -291,43 +294,28 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   }
   griddep_wait();
   griddep_launch_dependents();
-  if (!STATES && a.cu && blockIdx.x == 0 && h == 0 && blockIdx.z == 0 && warp == 0) decay_check_offsets(a);
-  const float g = a.g[h];
-  // tile row i holds scan position i of the chunk, or 127 - i where a reversed scan's tiles stay in memory order
-  const bool rev = FETCH != kFetchTokens && (p.mode & 1);
-  DecayUnit u_;
-  bool on = decay_unit(a, blockIdx.x, u_);
-  if (tid < C + kSteps) {
-    // threads C ..: lambda to the tokens of a whole chunk, of the last one, of either where its first token counts
-    // without its decay (lag), and of a segment
-    const int last = on ? u_.n - max(u_.n - 1, 0) / C * C : 0;
-    const int i = tid <= C ? tid : (tid == C + kLast ? last : (tid == C + kFullLag ? C - 1 : (tid == C + kLastLag ? max(last - 1, 0) : a.seg)));
-    const float2 w = decay_pow(g, i);
-    if (tid <= C) sh.pw[tid] = w.x;
-    if (tid >= C) sh.step[tid - C] = w;
-    if (tid < 16) sh.p16[rev ? tid : 15 - tid] = w.x;
-    if (tid < 32) sh.pa[tid] = p.a * w.x;
-  }
-  if (STATES && on) on = u_.nseg > 1 && u_.i < u_.nseg - 1;  // a last segment's state is formed by the output pass
+  if (!STATES && a.cu && blockIdx.x == 0 && warp == 0) decay_check_offsets(a);
+  bool on = true;
   if (sb & 1023u) {  // the swizzled tiles start at 1024-byte boundaries
-    set_status(a.status, DIG_ERR_CUDA);
+    if (tid == 0) set_status(a.status, DIG_ERR_CUDA);
     on = false;
   }
-  if (tid == 0) sh.u = u_;
+  if (warp == 0) {
+    const long long per = a.cu ? deal_total(a) : (long long)a.B * a.deal.chunks;
+    if (ln == 0) {
+      const long long grains = per * a.H * a.deal.nprob / a.deal.gran;
+      const int grid = (int)min((long long)a.deal.grid, grains), i = blockIdx.x;
+      sh.per = per;
+      sh.grains = grains;
+      sh.grid = grid;
+      sh.at = on && i < grid ? i * grains / grid * a.deal.gran : 0;
+      sh.end = on && i < grid ? (i + 1) * grains / grid * a.deal.gran : 0;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const DecayUnit& u = sh.u;
   const uint32_t tmem = sh.tmem;
-  if (!on) {
-    if (warp == W0) tmem_dealloc(tmem, F::TM_COLS);
-    return;
-  }
-  const int nch = (u.n + C - 1) / C;
-  const int terms = p.Sf && u.slot >= 0 ? 3 : 2;  // of khat
-  const int kk = (p.dk + 15) / 16;                // K-steps over the key channels
-  const int nv = (p.dv + 15) / 16 * 16;           // columns of the products with v or S
-  auto tile = [&](int x, int m) { return sb + ((m & 1) * F::PER + x) * F::TILE; };  // x: 0 k, 1 v, 2 q
   // Waits are bounded; after one gave up every other one does, nothing more is issued and the block leaves.
   bool timed_out = false;
   auto wait_bar = [&](uint64_t* bar, uint32_t parity) {
@@ -336,12 +324,81 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     return !timed_out;
   };
 
-  if (warp >= W0) {
-   if constexpr (F::SMALL) regs_down<kSmallServiceRegs>();
-   if (warp == W0) {
+  // Every role walks the pieces; block-wide barriers part them.  next_piece: the piece and the tables of its head (formed
+  // by the workers); false: no more.
+  auto next_piece = [&](bool worker) {
+    if (warp == 0) {
+      long long r = sh.at;
+      const long long r1 = sh.end;
+      bool more = r < r1;
+      if (more) {
+        DecayPiece piece;
+        if (STATES) {  // the last unit's, if it goes on in the next block
+          decay_piece(a, sh.per, r1 - 1, r1, piece);
+          r = max(r, piece.unit_start);
+        }
+        decay_piece(a, sh.per, r, r1, piece);
+        if (STATES) more = !piece.last;
+        __syncwarp();
+        if (ln == 0) {
+          sh.u = piece;
+          sh.g = a.g[piece.h];
+          sh.keep = a.p[piece.z].Sf && piece.slot >= 0;
+          sh.at = STATES ? r1 : r + piece.chunks;
+        }
+      }
+      if (ln == 0) sh.more = more;
+    }
+    named_bar(0, NT + 128);
+    if (!sh.more) return false;
+    if (worker && tid < C + kSteps) {
+      const DecayPiece& u = sh.u;
+      const DecayProblem& p = a.p[u.z];
+      const float g = sh.g;
+      // threads C ..: lambda to the tokens of a whole chunk, of the last one, of either where its first token counts
+      // without its decay (lag), and of the shorter and the longer of the blocks' runs
+      const int last = u.n - max(u.n - 1, 0) / C * C;
+      const long long i = tid <= C             ? tid
+                          : tid == C + kLast    ? last
+                          : tid == C + kFullLag ? C - 1
+                          : tid == C + kLastLag ? max(last - 1, 0)
+                                                : (sh.grains / sh.grid + (tid - C - kRun)) * C;
+      const float2 w = decay_pow(g, i);
+      if (tid <= C) sh.pw[tid] = w.x;
+      if (tid >= C) sh.step[tid - C] = w;
+      if (tid < 16) sh.p16[FETCH != kFetchTokens && (p.mode & 1) ? tid : 15 - tid] = w.x;
+      if (tid < 32) sh.pa[tid] = p.a * w.x;
+    }
+    named_bar(0, NT + 128);
+    return true;
+  };
+  // Every role is through with the piece; false: one gave up.
+  auto piece_done = [&]() {
+    named_bar(0, NT + 128);
+    return *reinterpret_cast<volatile int*>(&sh.abort) == 0;
+  };
+  auto tile = [&](int x, int m) { return sb + ((m & 1) * F::PER + x) * F::TILE; };  // x: 0 k, 1 v, 2 q
+  const DecayPiece& u = sh.u;
+  // a value that every lane has, as one the compiler knows to be the same in all of them
+  auto same = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+  // bf16 terms of khat in the chunk from which on `left` tokens of the piece are left
+  auto terms_of = [&](int left) {
+    const int after = u.len - u.t0 - u.n + left - C;  // tokens of the sequence after the chunk
+    return same(sh.keep && sh.g * max(after, 0) >= -7.f ? 3 : 2);
+  };
+  int base = 0;  // chunks before this piece: they are counted through the pieces
+
+  if (warp == W0) {
     // ---- the issuing warp
+    regs_down<F::SERVICE_REGS>();
     const uint32_t one = elect_one();
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    while (next_piece(false)) {
+    const DecayProblem& p = a.p[same(u.z)];
+    const int end = base + same((u.n + C - 1) / C);
+    const int kk = (p.dk + 15) / 16;       // K-steps over the key channels
+    const int nv = (p.dv + 15) / 16 * 16;  // columns of the products with v or S
+    int left = same(u.n);                  // tokens from the current chunk on
     const uint32_t id_qk = idesc_bf16(128, 128), id_v = idesc_bf16(128, nv, false, true);
     const uint64_t s_desc = mn_desc(sb + F::OFF_S, F::S_ATOM);
     auto kstep = [](int ks) { return (uint64_t)(((ks >> 2) * F::ATOM + (ks & 3) * 32) >> 4); };
@@ -354,10 +411,11 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     };
     constexpr bool AHEAD = !STATES && !F::SMALL;  // q k^T of a chunk follows P v of the one before
     auto ready = [&](int x, int m) { return __all_sync(0xFFFFFFFFu, wait_bar(&sh.full[x][m & 1], (m >> 1) & 1)); };
-    if (AHEAD && nch > 0 && ready(0, 0) && ready(2, 0)) qk(0);
+    if (AHEAD && end > base && ready(0, base) && ready(2, base)) qk(base);
 #pragma unroll 1
-    for (int m = 0; m < nch; ++m) {
+    for (int m = base; m < end; ++m, left -= C) {
       const uint32_t ph = m & 1;
+      const int terms = terms_of(left);
       if (!ready(1, m) || !__all_sync(0xFFFFFFFFu, wait_bar(&sh.bar_k, ph))) break;
       tc_fence_after();
       const uint64_t v0 = mn_desc(tile(1, m), F::ATOM);
@@ -392,27 +450,35 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           for (int ks = 0; ks < C / 16; ++ks)
             mma_ts(one, tm + F::TM_O2, tm + F::TM_P + 16 * ks + 8 * i, v0 + (uint64_t)((2048 * ks) >> 4), id_v, i == 1 && ks == 0 ? 0u : 1u);
         commit(one, &sh.bar_pv);
-        if (AHEAD && m + 1 < nch) {
+        if (AHEAD && m + 1 < end) {
           if (!ready(0, m + 1) || !ready(2, m + 1)) break;
           qk(m + 1);
         }
       }
     }
+    base = end;
+    if (!piece_done()) break;
+    }
     commit(one, &sh.bar_end);  // no product outlives the block
     mbar_wait(&sh.bar_end, 0, kSpinLimitNs);
-    __syncwarp();
-   } else {
+  } else if (warp > W0) {
     // ---- the fetching warps: tile x of each chunk, in 16-byte pieces where all strides allow it, else in 8-byte ones
+    regs_down<F::SERVICE_REGS>();
     const int x = warp - W0 - 1;
+    uint32_t cleaned = 0;  // pieces whose last tiles this warp has cleaned
+    while (next_piece(false)) {
+    const DecayProblem& p = a.p[same(u.z)];
+    const int h = same(u.h), end = base + same((u.n + C - 1) / C);
+    const bool rev = FETCH != kFetchTokens && (p.mode & 1);
     if (x < F::PER) {
       const bool wide = (p.dk | p.dv) % 8 == 0 && (p.qs | p.ks | p.vs) % 8 == 0 &&
                         ((reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v)) & 15) == 0;
       const int d = x == 1 ? p.dv : p.dk;
       const long long st = 2 * (x == 0 ? p.ks : (x == 1 ? p.vs : p.qs));
-      const char* base = static_cast<const char*>(x == 0 ? p.k : (x == 1 ? p.v : p.q)) + (size_t)h * d * 2;
+      const char* src0 = static_cast<const char*>(x == 0 ? p.k : (x == 1 ? p.v : p.q)) + (size_t)h * d * 2;
       auto fetch = [&](int m) {
         const uint32_t dst = tile(x, m);
-        const int n = min(C, u.n - m * C);
+        const int n = min(C, u.n - (m - base) * C);
         if (x == 0) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -429,7 +495,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           __syncwarp();
           if (ln == 0) {
             mbar_arrive_expect_tx(bar, atoms * F::ATOM);
-            const int t0 = u.t0 + m * C;
+            const int t0 = u.t0 + (m - base) * C;
             if constexpr (FETCH == kFetchRows) {
               const int r = (rev ? u.len - t0 - C : t0) + (a.cu ? u.first : 0);
               for (int i = 0; i < atoms; ++i) tma_load_5d(dst + i * F::ATOM, map, 64 * i, h, r, a.cu ? 0 : u.b, 0, bar);
@@ -445,7 +511,8 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
             }
           }
           if (clean) {
-            wait_bar(&sh.landed[x], 0);
+            wait_bar(&sh.landed[x], cleaned & 1);
+            ++cleaned;
             const int r0 = rev ? 0 : n, rows = C - n;
             for (int i = ln; i < rows * 8; i += 32)
               for (int j = 0; j < atoms; ++j) sts128(dst + j * F::ATOM + (r0 + i / 8) * 128 + (i % 8) * 16, 0, 0, 0, 0);
@@ -457,7 +524,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         int row[4];  // of tokens ln, ln + 32, ..
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int s = m * C + 32 * i + ln;
+          const int s = (m - base) * C + 32 * i + ln;
           row[i] = s < u.n ? decay_row(a, u, p.mode, u.t0 + s) : -1;
         }
         auto go = [&](auto bytes) {
@@ -466,7 +533,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           const bool any = c < (d + 15) / 16 * 16, in = c < d;  // columns that a product reads; that exist
           const uint32_t cdst = dst + (c >> 6) * F::ATOM + (N == 16 ? 0u : (c & 4) * 2u);
           const int ch = (c & 63) >> 3;
-          const char* cb = base + 2 * c;
+          const char* cb = src0 + 2 * c;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll 2
@@ -474,7 +541,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
               const int r = r0 + ln / PR;
               const int gr = __shfl_sync(0xFFFFFFFFu, row[i], r);
               const bool ok = in && gr >= 0;
-              if (any) cp_piece<N>(cdst + (32 * i + r) * 128 + ((ch ^ (r & 7)) << 4), ok ? cb + gr * st : base, ok ? N : 0);
+              if (any) cp_piece<N>(cdst + (32 * i + r) * 128 + ((ch ^ (r & 7)) << 4), ok ? cb + gr * st : src0, ok ? N : 0);
             }
         };
         if (wide) go(std::integral_constant<int, 16>{});
@@ -487,17 +554,19 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         }
       };
 #pragma unroll 1
-      for (int m = 0; m < nch; ++m) {
+      for (int m = base; m < end; ++m) {
         if (m >= 2 && __any_sync(0xFFFFFFFFu, !wait_bar(&sh.free_[x][m & 1], ((m - 2) >> 1) & 1))) break;
         fetch(m);
       }
     }
-   }
+    base = end;
+    if (!piece_done()) break;
+    }
   } else {
-    if constexpr (F::SMALL) regs_up<kSmallWorkerRegs>();
+    // ---- the workers
+    regs_up<F::WORKER_REGS>();
     const int t = tid & 127, cg = tid >> 7;  // token row or key channel (the thread's TMEM lane); column group
     const uint32_t lane = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const bool key = t < D && t < p.dk;      // this lane holds a key channel of the state
     auto arrive = [&](uint64_t* bar) {       // the warp's writes to tensor and shared memory are done
       fence_async_smem();
       tc_fence_before();
@@ -505,18 +574,22 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       if (ln == 0) mbar_arrive(bar);
     };
 
-    // ---- the state the segment starts from: lane t = key channel, value channels 32 cg ..
+    while (next_piece(true)) {
+    const DecayProblem& p = a.p[same(u.z)];
+    const int h = same(u.h);
+    // tile row i holds scan position i of the chunk, or 127 - i where a reversed scan's tiles stay in memory order
+    const bool rev = FETCH != kFetchTokens && (p.mode & 1);
+    const int kk = (p.dk + 15) / 16;                // K-steps over the key channels
+    const int nv = (p.dv + 15) / 16 * 16;           // columns of the products with v or S
+    const bool key = t < D && t < p.dk;             // this lane holds a key channel of the state
+    // ---- the state the piece starts from: lane t = key channel, value channels 32 cg ..
     float S[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) S[j] = 0.f;
-    float* seg_base = a.segst + blockIdx.z * a.segst_problem;
-    const int seg0 = blockIdx.x - u.i;
-    // element (c, j) of a segment state: four value channels of consecutive key channels side by side
-    auto seg_state = [&](int sidx) {
-      return reinterpret_cast<float4*>(seg_base + ((size_t)sidx * a.H + h) * (D * D)) + (cg * 8) * D + t;
-    };
+    // element (c, j) of a block's state: four value channels of consecutive key channels side by side
+    auto block_state = [&](int i) { return reinterpret_cast<float4*>(a.segst + (size_t)i * (D * D)) + (cg * 8) * D + t; };
     if (t < D) {
-      if (u.i == 0 && (STATES || u.nseg == 1)) {
+      if (u.t0 == 0 && (STATES || u.last)) {
         if (p.S0 && u.slot >= 0 && key) {
           const float* s0 = p.S0 + ((size_t)u.slot * a.H + h) * p.dk * p.dv;
           if (p.s0_t) {
@@ -532,18 +605,21 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
               }
           }
         }
-      } else if (!STATES && u.i == 0) {  // the copy of S0 that the first pass left (S0 may be overwritten by the last segment)
-        const float4* s0 = seg_state(seg0 + u.nseg - 1);
+        if (STATES) {  // a copy for the second pass, in which the unit's last block may already have written S_final there
+          float4* s0 = block_state(a.deal.grid + blockIdx.x);
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 x = s0[(j / 4) * D];
-          S[j] = x.x, S[j + 1] = x.y, S[j + 2] = x.z, S[j + 3] = x.w;
+          for (int j = 0; j < 32; j += 4) s0[(j / 4) * D] = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
         }
       } else if (!STATES) {
-        const float2 w = sh.step[kSegment];
+        // the states of the blocks that have walked the unit so far; at its start, the copy of S0
+        int j0 = blockIdx.x, j1 = blockIdx.x;
+        const int grid = sh.grid, rem = (int)(sh.grains % grid);
+        if (u.t0 > 0) j0 = (int)(((u.unit_start + 1) * grid - 1) / sh.grains);
+        else j0 = a.deal.grid + blockIdx.x, j1 = j0 + 1;
 #pragma unroll 2
-        for (int m = 0; m < u.i; ++m) {
-          const float4* ls = seg_state(seg0 + m);
+        for (int i = j0; i < j1; ++i) {
+          const float4* ls = block_state(i);
+          const float2 w = sh.step[(int)((long long)(i + 1) * rem / grid - (long long)i * rem / grid) ? kRun1 : kRun];
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             const float4 x = ls[(j / 4) * D];
@@ -554,12 +630,8 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           }
         }
       }
-      if (STATES && u.i == 0) {
-        float4* s0 = seg_state(seg0 + u.nseg - 1);  // the last segment's place is free: it leaves no state there
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) s0[(j / 4) * D] = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
-      }
     }
+    int left = same(u.n);  // tokens from the current chunk on
     // S in bf16, rows = key channels (64 value channels each), the second operand of q S
     auto put_state = [&]() {
       if (t < D) {
@@ -574,7 +646,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     if constexpr (!STATES) put_state();
     // khat^T of chunk m -> tensor memory: the warp's 32 channels, its group's tokens.  LAST: the last of three terms alone,
     // formed again once its place is free (held in registers meanwhile it would push others out to local memory).
-    auto convert_k = [&](int m, auto last) {
+    auto convert_k = [&](int m, int terms, auto last) {
       constexpr bool LAST = decltype(last)::value;
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
@@ -694,9 +766,9 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       fence_async_smem();
       named_bar(5 + (warp & 3), 32 * CG);
       if (storer) {
-        const CUtensorMap& map = a.omap[blockIdx.z];
+        const CUtensorMap& map = a.omap[u.z];
         const uint32_t src = tile(1, m) + warp * 4096;
-        const int atoms = (p.dv + 63) / 64, t0 = u.t0 + m * C, i0 = 32 * warp;
+        const int atoms = (p.dv + 63) / 64, t0 = u.t0 + u.n - left, i0 = 32 * warp;
         if constexpr (FETCH == kFetchRows) {
           const int r = (rev ? u.len - t0 - C : t0) + i0 + (a.cu ? u.first : 0);
           for (int i = 0; i < atoms; ++i) tma_store_5d(map, 64 * i, h, r, a.cu ? 0 : u.b, 0, src + i * F::ATOM);
@@ -737,7 +809,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         sts128(st + swz_off<64>(ln, j / 8 + 1), w[4], w[5], w[6], w[7]);
       }
       __syncwarp();
-      const int row = m * C + s < u.n ? decay_row(a, u, p.mode, u.t0 + m * C + s) : -1;
+      const int row = s < left ? decay_row(a, u, p.mode, u.t0 + u.n - left + s) : -1;
       char* o = static_cast<char*>(p.o) + ((size_t)h * p.dv + jj) * 2;
       const size_t os = (size_t)a.H * p.dv * 2;
       const int left = p.dv - jj;
@@ -761,50 +833,55 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     if constexpr (STATES) {
       // khat of the next chunk is formed while the tensor core sums this one's dS (D = 128: two places for it)
       constexpr bool AHEAD = !F::SMALL;
-      for (int m = 0; m < nch + (AHEAD ? 1 : 0); ++m) {
-        if (m < nch) {
+      const int end = base + same((u.n + C - 1) / C);
+#pragma unroll 1
+      for (int m = base; m < end + (AHEAD ? 1 : 0); ++m) {
+        if (m < end) {
           wait_bar(&sh.full[0][m & 1], (m >> 1) & 1);
           if (__any_sync(0xFFFFFFFFu, timed_out || *reinterpret_cast<volatile int*>(&sh.abort))) break;
-          convert_k(m, kAll);
+          convert_k(m, terms_of(left - (AHEAD && m > base ? C : 0)), kAll);
         }
         const int j = AHEAD ? m - 1 : m;
         if (!AHEAD) arrive(&sh.bar_k);
-        if (j >= 0) {
+        if (j >= base) {
           wait_bar(&sh.bar_ds, j & 1);
           tc_fence_after();
-          update(min(C, u.n - j * C), p.lag && u.t0 + j * C == 0 ? 1 : 0);
+          update(min(C, left), p.lag && u.t0 == 0 && j == base ? 1 : 0);
+          left -= C;
         }
-        if (AHEAD && m < nch) arrive(&sh.bar_k);
+        if (AHEAD && m < end) arrive(&sh.bar_k);
       }
+      base = end;
       if (t < D) {
-        float4* out = seg_state(blockIdx.x);
+        float4* out = block_state(blockIdx.x);
 #pragma unroll
         for (int j = 0; j < 32; j += 4) out[(j / 4) * D] = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
       }
     } else {
       auto full = [&](int m) { wait_bar(&sh.full[0][m & 1], (m >> 1) & 1); };
-      if (!F::SMALL && nch > 0) {
-        full(0);
-        convert_k(0, kAll);
+      if (!F::SMALL && left > 0) {
+        full(base);
+        convert_k(base, terms_of(left), kAll);
       }
 #pragma unroll 1
-      for (int m = 0; m < nch; ++m) {
+      for (int m = base; left > 0; ++m, left -= C) {
         const uint32_t ph = m & 1;
-        const int n = min(C, u.n - m * C);
-        const int e = (p.lag && u.t0 + m * C == 0) ? 1 : 0;
+        const int n = min(C, left);
+        const int e = (p.lag && u.t0 == 0 && left == u.n) ? 1 : 0;
+        const int terms = terms_of(left);
         if (F::SMALL) full(m);
         // khat (D = 128: its third term) comes over the last chunk's outputs, once the warps of these lanes have read them
         const bool stop = timed_out || *reinterpret_cast<volatile int*>(&sh.abort);
         if (F::SMALL || terms == 3 ? bar_or(1 + (warp & 3), 32 * CG, stop) : (bool)__any_sync(0xFFFFFFFFu, stop)) break;
-        if (F::SMALL) convert_k(m, kAll);
-        else if (terms == 3) convert_k(m, kThird);
+        if (F::SMALL) convert_k(m, terms, kAll);
+        else if (terms == 3) convert_k(m, terms, kThird);
         arrive(&sh.bar_k);
         if (!F::SMALL) {
           wait_bar(&sh.bar_qk, ph);
           tc_fence_after();
           convert_p();
         }
-        if (FETCH != kFetchTokens && m > 0) put_done(m - 1);
+        if (FETCH != kFetchTokens && left != u.n) put_done(m - 1);
         wait_bar(&sh.bar_ds, ph);
         tc_fence_after();
         update(n, e);  // before P v, which comes to stand in dS's place
@@ -816,9 +893,9 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         arrive(&sh.bar_p);
         wait_bar(&sh.bar_qs, ph);
         put_state();
-        if (!F::SMALL && m + 1 < nch) {  // while the tensor core is at P v
+        if (!F::SMALL && left > C) {  // while the tensor core is at P v
           full(m + 1);
-          convert_k(m + 1, kAll);
+          convert_k(m + 1, terms_of(left - C), kAll);
         }
         wait_bar(&sh.bar_pv, ph);
         tc_fence_after();
@@ -826,15 +903,13 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           put_tma(m, e);
         } else {
           put_out(m, e);
-          if (FETCH == kFetchTokens) {  // (elsewhere only a segment's last chunk comes here, over whose tile nothing is fetched)
-            fence_async_smem();
-            named_bar(5 + (warp & 3), 32 * CG);
-            put_done(m);
-          }
+          fence_async_smem();  // the next tile comes over what was staged there
+          named_bar(5 + (warp & 3), 32 * CG);
         }
+        if (FETCH == kFetchTokens || left <= C) put_done(m);
       }
-      if (FETCH != kFetchTokens && storer) bulk_wait_all();
-      if (p.Sf && u.slot >= 0 && u.i == u.nseg - 1 && key) {
+      base += same((u.n + C - 1) / C);
+      if (p.Sf && u.slot >= 0 && u.last && key) {
         // dS0 = lambda G_0; an empty sequence passes its state on as it is
         const float w = p.lag && u.len > 0 ? sh.pw[1] : 1.f;
         float* out = p.Sf + ((size_t)u.slot * a.H + h) * p.dk * p.dv + (size_t)t * p.dv + cg * 32;
@@ -843,6 +918,9 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           if (cg * 32 + j < p.dv) *reinterpret_cast<float4*>(out + j) = make_float4(w * S[j], w * S[j + 1], w * S[j + 2], w * S[j + 3]);
       }
     }
+    if (!piece_done()) break;
+    }
+    if (!STATES && FETCH != kFetchTokens && warp < 4) bulk_wait_all();
   }
   if (timed_out) set_status(a.status, DIG_ERR_DEVICE_TIMEOUT);
   tc_fence_before();
@@ -852,30 +930,29 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
 }
 
 template <int D, bool STATES, int FETCH>
-cudaError_t run(const DecayArgs& a, dim3 grid, cudaStream_t s) {
+cudaError_t run(const DecayArgs& a, cudaStream_t s) {
   using F = TcCfg<D, STATES>;
   constexpr int smem = F::OFF_T + sizeof(TcTables);
   const cudaError_t e = cudaFuncSetAttribute(decay_tc_kernel<D, STATES, FETCH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decay_tc_kernel<D, STATES, FETCH>, grid, dim3(F::NT + 128), smem, s, a);
+  return launch_pdl(decay_tc_kernel<D, STATES, FETCH>, dim3(a.deal.grid), dim3(F::NT + 128), smem, s, a);
 }
 
 template <int D, int FETCH>
-cudaError_t passes(const DecayArgs& a, dim3 grid, bool multi, cudaStream_t s) {
+cudaError_t passes(const DecayArgs& a, bool multi, cudaStream_t s) {
   cudaError_t e;
-  if (multi && (e = run<D, true, FETCH>(a, grid, s)) != cudaSuccess) return e;
-  return run<D, false, FETCH>(a, grid, s);
+  if (multi && (e = run<D, true, FETCH>(a, s)) != cudaSuccess) return e;
+  return run<D, false, FETCH>(a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_decay_tc(const DecayArgs& a, int nprob, int nseg_total, bool multi, int D, cudaStream_t s) {
-  const dim3 grid(nseg_total, a.H, nprob);
+cudaError_t launch_decay_tc(const DecayArgs& a, bool multi, int D, cudaStream_t s) {
   auto go = [&](auto d) {
     constexpr int DD = decltype(d)::value;
-    return a.fetch == kFetchRows   ? passes<DD, kFetchRows>(a, grid, multi, s)
-           : a.fetch == kFetchCols ? passes<DD, kFetchCols>(a, grid, multi, s)
-                                   : passes<DD, kFetchTokens>(a, grid, multi, s);
+    return a.fetch == kFetchRows   ? passes<DD, kFetchRows>(a, multi, s)
+           : a.fetch == kFetchCols ? passes<DD, kFetchCols>(a, multi, s)
+                                   : passes<DD, kFetchTokens>(a, multi, s);
   };
   return D == 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
 }
