@@ -220,7 +220,7 @@ struct TcCfg {
   static constexpr int PER = STATES ? 2 : 3;      // tiles of a chunk: k, v, q
   static constexpr int S_ATOM = D * 128;
   static constexpr int OFF_S = PER * 2 * TILE;
-  static constexpr int OFF_T = OFF_S + (STATES ? 0 : S_ATOM * (D / 64));
+  static constexpr int OFF_T = OFF_S + S_ATOM * (D / 64);
   // Registers: 512 x 104 + 128 x 56 of 640 x 96 (D = 128), 256 x 96 + 128 x 48 of 384 x 80 (D = 64).  What does not fit goes
   // to local memory, for which little L1 is left beside the tiles: a load from there costs a trip to L2.
   static constexpr int WORKER_REGS = SMALL ? 96 : 104, SERVICE_REGS = SMALL ? 48 : 56;
@@ -237,23 +237,30 @@ struct TcCfg {
   }
 };
 
+// A piece and what its chunks need of its head's decay.
+struct TcPiece {
+  float pw[C + 4];            // lambda^i
+  float pa[32];               // a lambda^i
+  alignas(16) float p16[16];  // lambda^(15-i), mirrored tiles: lambda^i
+  float2 step[kSteps];        // lambda^i = hi + lo of a chunk's or a block's run of tokens
+  DecayPiece u;
+  float g;                    // the head's log decay
+  int keep;                   // whether the unit's final state is asked for
+  int j0;                     // the block that began the unit
+  int more;                   // 0: there is no such piece
+};
+
 struct TcTables {
-  float pw[C + 4];                  // lambda^i
-  float2 step[kSteps];              // lambda^i = hi + lo of a chunk's or a block's run of tokens
-  float pa[32];                     // a lambda^i
-  alignas(16) float p16[16];        // lambda^(15-i), mirrored tiles: lambda^i
+  TcPiece piece[2];
   float wk[2][C];                   // b lambda^(n-1-s) of chunk m in m & 1, 0 past its end
   uint64_t full[3][2];              // tile x (k, v, q) of the chunk has come
   uint64_t landed[2];               // k and v of a chunk that ends inside its tiles
   uint64_t free_[3][2];             // tile x (k, v, q) of the chunk is no longer read
   uint64_t bar_k, bar_p;            // the workers': khat (with S) written, P written (and dS read)
   uint64_t bar_qk, bar_ds, bar_qs, bar_pv, bar_end;  // the tensor core's
-  DecayPiece u;
-  float g;    // the head's log decay
-  int keep;   // whether the unit's final state is asked for
-  // how the chunks are dealt, and what of this block's run is left (kept here: registers are short)
+  // how the chunks are dealt, and what of this block's run is left
   long long per, grains, at, end;
-  int grid, more;
+  int grid;
   uint32_t tmem;
   int abort;
 };
@@ -300,18 +307,6 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     if (tid == 0) set_status(a.status, DIG_ERR_CUDA);
     on = false;
   }
-  if (warp == 0) {
-    const long long per = a.cu ? deal_total(a) : (long long)a.B * a.deal.chunks;
-    if (ln == 0) {
-      const long long grains = per * a.H * a.deal.nprob / a.deal.gran;
-      const int grid = (int)min((long long)a.deal.grid, grains), i = blockIdx.x;
-      sh.per = per;
-      sh.grains = grains;
-      sh.grid = grid;
-      sh.at = on && i < grid ? i * grains / grid * a.deal.gran : 0;
-      sh.end = on && i < grid ? (i + 1) * grains / grid * a.deal.gran : 0;
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -324,67 +319,78 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     return !timed_out;
   };
 
-  // Every role walks the pieces; block-wide barriers part them.  next_piece: the piece and the tables of its head (formed
-  // by the workers); false: no more.
-  auto next_piece = [&](bool worker) {
-    if (warp == 0) {
-      long long r = sh.at;
-      const long long r1 = sh.end;
-      bool more = r < r1;
-      if (more) {
-        DecayPiece piece;
-        if (STATES) {  // the last unit's, if it goes on in the next block
-          decay_piece(a, sh.per, r1 - 1, r1, piece);
-          r = max(r, piece.unit_start);
-        }
-        decay_piece(a, sh.per, r, r1, piece);
-        if (STATES) more = !piece.last;
-        __syncwarp();
-        if (ln == 0) {
-          sh.u = piece;
-          sh.g = a.g[piece.h];
-          sh.keep = a.p[piece.z].Sf && piece.slot >= 0;
-          sh.at = STATES ? r1 : r + piece.chunks;
-        }
+  // Every role walks the pieces, parted by block-wide barriers; one warp plans the next while this one is walked.
+  auto plan = [&](int k) {
+    TcPiece& t = sh.piece[k & 1];
+    if (k == 0) {
+      const long long per = a.cu ? deal_total(a) : (long long)a.B * a.deal.chunks;
+      const long long grains = per * a.H * a.deal.nprob / a.deal.gran;
+      const int grid = (int)min((long long)a.deal.grid, grains), i = blockIdx.x;
+      if (ln == 0) {
+        sh.per = per;
+        sh.grains = grains;
+        sh.grid = grid;
+        sh.at = on && i < grid ? i * grains / grid * a.deal.gran : 0;
+        sh.end = on && i < grid ? (i + 1) * grains / grid * a.deal.gran : 0;
       }
-      if (ln == 0) sh.more = more;
+      __syncwarp();
     }
-    named_bar(0, NT + 128);
-    if (!sh.more) return false;
-    if (worker && tid < C + kSteps) {
-      const DecayPiece& u = sh.u;
+    long long r = sh.at;
+    const long long r1 = sh.end;
+    bool more = r < r1;
+    if (more) {
+      DecayPiece u;
+      if (STATES) {  // the last unit's, if it goes on in the next block
+        decay_piece(a, sh.per, r1 - 1, r1, u);
+        r = max(r, u.unit_start);
+      }
+      decay_piece(a, sh.per, r, r1, u);
+      if (STATES) more = !u.last;
       const DecayProblem& p = a.p[u.z];
-      const float g = sh.g;
-      // threads C ..: lambda to the tokens of a whole chunk, of the last one, of either where its first token counts
-      // without its decay (lag), and of the shorter and the longer of the blocks' runs
-      const int last = u.n - max(u.n - 1, 0) / C * C;
-      const long long i = tid <= C             ? tid
-                          : tid == C + kLast    ? last
-                          : tid == C + kFullLag ? C - 1
-                          : tid == C + kLastLag ? max(last - 1, 0)
-                                                : (sh.grains / sh.grid + (tid - C - kRun)) * C;
-      const float2 w = decay_pow(g, i);
-      if (tid <= C) sh.pw[tid] = w.x;
-      if (tid >= C) sh.step[tid - C] = w;
-      if (tid < 16) sh.p16[FETCH != kFetchTokens && (p.mode & 1) ? tid : 15 - tid] = w.x;
-      if (tid < 32) sh.pa[tid] = p.a * w.x;
+      const float g = a.g[u.h];
+      if (ln == 0) {
+        t.u = u;
+        t.g = g;
+        t.keep = p.Sf && u.slot >= 0;
+        t.j0 = (int)(((u.unit_start + 1) * sh.grid - 1) / sh.grains);
+        sh.at = STATES ? r1 : r + u.chunks;
+      }
+      const bool rev = FETCH != kFetchTokens && (p.mode & 1);
+      const long long run = sh.grains / sh.grid;
+#pragma unroll 1
+      for (int j = ln; j < C + kSteps; j += 32) {
+        // from C on: lambda to the tokens of a whole chunk, of the last one, of either where its first token counts
+        // without its decay (lag), and of the shorter and the longer of the blocks' runs
+        const int last = u.n - max(u.n - 1, 0) / C * C;
+        const long long i = j <= C             ? j
+                            : j == C + kLast    ? last
+                            : j == C + kFullLag ? C - 1
+                            : j == C + kLastLag ? max(last - 1, 0)
+                                                : (run + (j - C - kRun)) * C;
+        const float2 w = decay_pow(g, i);
+        if (j <= C) t.pw[j] = w.x;
+        if (j >= C) t.step[j - C] = w;
+        if (j < 16) t.p16[rev ? j : 15 - j] = w.x;
+        if (j < 32) t.pa[j] = p.a * w.x;
+      }
     }
-    named_bar(0, NT + 128);
-    return true;
+    if (ln == 0) t.more = more;
+    __syncwarp();
   };
+  if (warp == W0 + 3) plan(0);
+  __syncthreads();
   // Every role is through with the piece; false: one gave up.
   auto piece_done = [&]() {
     named_bar(0, NT + 128);
     return *reinterpret_cast<volatile int*>(&sh.abort) == 0;
   };
   auto tile = [&](int x, int m) { return sb + ((m & 1) * F::PER + x) * F::TILE; };  // x: 0 k, 1 v, 2 q
-  const DecayPiece& u = sh.u;
   // a value that every lane has, as one the compiler knows to be the same in all of them
   auto same = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
   // bf16 terms of khat in the chunk from which on `left` tokens of the piece are left
-  auto terms_of = [&](int left) {
-    const int after = u.len - u.t0 - u.n + left - C;  // tokens of the sequence after the chunk
-    return same(sh.keep && sh.g * max(after, 0) >= -7.f ? 3 : 2);
+  auto terms_of = [&](const TcPiece& t, int left) {
+    const int after = t.u.len - t.u.t0 - t.u.n + left - C;  // tokens of the sequence after the chunk
+    return same(t.keep && t.g * max(after, 0) >= -7.f ? 3 : 2);
   };
   int base = 0;  // chunks before this piece: they are counted through the pieces
 
@@ -393,7 +399,10 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     regs_down<F::SERVICE_REGS>();
     const uint32_t one = elect_one();
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-    while (next_piece(false)) {
+#pragma unroll 1
+    for (int piece = 0; sh.piece[piece & 1].more; ++piece) {
+    const TcPiece& tab = sh.piece[piece & 1];
+    const DecayPiece& u = tab.u;
     const DecayProblem& p = a.p[same(u.z)];
     const int end = base + same((u.n + C - 1) / C);
     const int kk = (p.dk + 15) / 16;       // K-steps over the key channels
@@ -415,7 +424,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
 #pragma unroll 1
     for (int m = base; m < end; ++m, left -= C) {
       const uint32_t ph = m & 1;
-      const int terms = terms_of(left);
+      const int terms = terms_of(tab, left);
       if (!ready(1, m) || !__all_sync(0xFFFFFFFFu, wait_bar(&sh.bar_k, ph))) break;
       tc_fence_after();
       const uint64_t v0 = mn_desc(tile(1, m), F::ATOM);
@@ -462,37 +471,37 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     commit(one, &sh.bar_end);  // no product outlives the block
     mbar_wait(&sh.bar_end, 0, kSpinLimitNs);
   } else if (warp > W0) {
-    // ---- the fetching warps: tile x of each chunk, in 16-byte pieces where all strides allow it, else in 8-byte ones
+    // ---- the fetching warps
     regs_down<F::SERVICE_REGS>();
-    const int x = warp - W0 - 1;
-    uint32_t cleaned = 0;  // pieces whose last tiles this warp has cleaned
-    while (next_piece(false)) {
+    uint32_t cleaned = 0;  // pieces whose last tiles were cleaned
+#pragma unroll 1
+    for (int piece = 0; sh.piece[piece & 1].more; ++piece) {
+    const TcPiece& tab = sh.piece[piece & 1];
+    const DecayPiece& u = tab.u;
     const DecayProblem& p = a.p[same(u.z)];
     const int h = same(u.h), end = base + same((u.n + C - 1) / C);
     const bool rev = FETCH != kFetchTokens && (p.mode & 1);
-    if (x < F::PER) {
-      const bool wide = (p.dk | p.dv) % 8 == 0 && (p.qs | p.ks | p.vs) % 8 == 0 &&
-                        ((reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v)) & 15) == 0;
-      const int d = x == 1 ? p.dv : p.dk;
-      const long long st = 2 * (x == 0 ? p.ks : (x == 1 ? p.vs : p.qs));
-      const char* src0 = static_cast<const char*>(x == 0 ? p.k : (x == 1 ? p.v : p.q)) + (size_t)h * d * 2;
-      auto fetch = [&](int m) {
-        const uint32_t dst = tile(x, m);
-        const int n = min(C, u.n - (m - base) * C);
-        if (x == 0) {
+    if (warp == W0 + 3) plan(piece + 1);
+    // the weights of khat in chunk m of n tokens
+    auto weights = [&](int m, int n) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int s = rev ? C - 1 - 32 * i - ln : 32 * i + ln;
-            sh.wk[m & 1][32 * i + ln] = s < n ? p.b * sh.pw[n - 1 - s] : 0.f;
-          }
-        }
-        if constexpr (FETCH != kFetchTokens) {
+      for (int i = 0; i < 4; ++i) {
+        const int s = rev ? C - 1 - 32 * i - ln : 32 * i + ln;
+        sh.wk[m & 1][32 * i + ln] = s < n ? p.b * tab.pw[n - 1 - s] : 0.f;
+      }
+      __syncwarp();
+    };
+    auto freed = [&](int x, int m) {  // the place of tile x of chunk m
+      return m < 2 || __all_sync(0xFFFFFFFFu, wait_bar(&sh.free_[x][m & 1], ((m - 2) >> 1) & 1));
+    };
+    if constexpr (FETCH != kFetchTokens) {
+      // one warp asks for a chunk's tiles in the order in which their places become free
+      if (warp == W0 + 1) {
+        auto fetch = [&](int x, int m, bool clean) {
+          const uint32_t dst = tile(x, m);
           const CUtensorMap& map = a.map[x == 0 ? p.mk : (x == 1 ? p.mv : p.mq)];
-          // packed: rows past the sequence's end are another's, and 0 times them need not be 0
-          const bool clean = x < 2 && a.cu && n < C;
           uint64_t* bar = clean ? &sh.landed[x] : &sh.full[x][m & 1];
-          const int atoms = min(D / 64, (d + 63) / 64);
-          __syncwarp();
+          const int atoms = min(D / 64, ((x == 1 ? p.dv : p.dk) + 63) / 64);
           if (ln == 0) {
             mbar_arrive_expect_tx(bar, atoms * F::ATOM);
             const int t0 = u.t0 + (m - base) * C;
@@ -500,7 +509,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
               const int r = (rev ? u.len - t0 - C : t0) + (a.cu ? u.first : 0);
               for (int i = 0; i < atoms; ++i) tma_load_5d(dst + i * F::ATOM, map, 64 * i, h, r, a.cu ? 0 : u.b, 0, bar);
             } else {
-              const int f0 = rev ? a.L - t0 - C : t0;  // a multiple of the run, as L and the segments are
+              const int f0 = rev ? a.L - t0 - C : t0;  // a multiple of the run, as L and the chunks are
               int col = f0 >= 0 ? f0 / a.Hg : 0, y = f0 >= 0 ? f0 - col * a.Hg : f0;
               for (int r = 0; r < C; r += kColRun) {
                 const int yy = y < 0 ? a.Hg : y;  // before the first token: off the grid, zeros
@@ -510,53 +519,83 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
               }
             }
           }
-          if (clean) {
-            wait_bar(&sh.landed[x], cleaned & 1);
-            ++cleaned;
-            const int r0 = rev ? 0 : n, rows = C - n;
-            for (int i = ln; i < rows * 8; i += 32)
-              for (int j = 0; j < atoms; ++j) sts128(dst + j * F::ATOM + (r0 + i / 8) * 128 + (i % 8) * 16, 0, 0, 0, 0);
-            fence_async_smem();
-            __syncwarp();
-            if (ln == 0) mbar_arrive(&sh.full[x][m & 1]);
-          }
-        } else {
-        int row[4];  // of tokens ln, ln + 32, ..
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int s = (m - base) * C + 32 * i + ln;
-          row[i] = s < u.n ? decay_row(a, u, p.mode, u.t0 + s) : -1;
-        }
-        auto go = [&](auto bytes) {
-          constexpr int N = decltype(bytes)::value, PR = D * 2 / N, RW = PR < 32 ? 32 / PR : 1;  // pieces of a row, rows at once
-          const int c = (ln % PR) * (N / 2);
-          const bool any = c < (d + 15) / 16 * 16, in = c < d;  // columns that a product reads; that exist
-          const uint32_t cdst = dst + (c >> 6) * F::ATOM + (N == 16 ? 0u : (c & 4) * 2u);
-          const int ch = (c & 63) >> 3;
-          const char* cb = src0 + 2 * c;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll 2
-            for (int r0 = 0; r0 < 32; r0 += RW) {
-              const int r = r0 + ln / PR;
-              const int gr = __shfl_sync(0xFFFFFFFFu, row[i], r);
-              const bool ok = in && gr >= 0;
-              if (any) cp_piece<N>(cdst + (32 * i + r) * 128 + ((ch ^ (r & 7)) << 4), ok ? cb + gr * st : src0, ok ? N : 0);
-            }
+          __syncwarp();
         };
-        if (wide) go(std::integral_constant<int, 16>{});
-        else go(std::integral_constant<int, 8>{});
-        cp_commit();
-        cp_wait<0>();
-        fence_async_smem();
-        __syncwarp();
-        if (ln == 0) mbar_arrive(&sh.full[x][m & 1]);
-        }
-      };
 #pragma unroll 1
-      for (int m = base; m < end; ++m) {
-        if (m >= 2 && __any_sync(0xFFFFFFFFu, !wait_bar(&sh.free_[x][m & 1], ((m - 2) >> 1) & 1))) break;
-        fetch(m);
+        for (int m = base; m < end; ++m) {
+          const int n = min(C, u.n - (m - base) * C);
+          // packed: rows past the sequence's end are another's, and 0 times them need not be 0
+          const bool clean = a.cu && n < C;
+          if (!freed(0, m)) break;
+          weights(m, n);
+          fetch(0, m, clean);
+          if (!STATES) {
+            if (!freed(2, m)) break;
+            fetch(2, m, false);
+          }
+          if (!freed(1, m)) break;
+          fetch(1, m, clean);
+          if (clean) {
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) {
+              wait_bar(&sh.landed[x], cleaned & 1);
+              const int r0 = rev ? 0 : n, atoms = min(D / 64, ((x == 1 ? p.dv : p.dk) + 63) / 64);
+#pragma unroll 1
+              for (int i = ln; i < (C - n) * 8; i += 32)
+                for (int j = 0; j < atoms; ++j) sts128(tile(x, m) + j * F::ATOM + (r0 + i / 8) * 128 + (i % 8) * 16, 0, 0, 0, 0);
+              fence_async_smem();
+              __syncwarp();
+              if (ln == 0) mbar_arrive(&sh.full[x][m & 1]);
+            }
+            ++cleaned;
+          }
+        }
+      }
+    } else {
+      // a warp per tile, in 16-byte pieces where all strides allow it, else in 8-byte ones
+      const int x = warp - W0 - 1;
+      if (x < F::PER) {
+        const bool wide = (p.dk | p.dv) % 8 == 0 && (p.qs | p.ks | p.vs) % 8 == 0 &&
+                          ((reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v)) & 15) == 0;
+        const int d = x == 1 ? p.dv : p.dk;
+        const long long st = 2 * (x == 0 ? p.ks : (x == 1 ? p.vs : p.qs));
+        const char* src0 = static_cast<const char*>(x == 0 ? p.k : (x == 1 ? p.v : p.q)) + (size_t)h * d * 2;
+#pragma unroll 1
+        for (int m = base; m < end; ++m) {
+          if (!freed(x, m)) break;
+          const uint32_t dst = tile(x, m);
+          if (x == 0) weights(m, min(C, u.n - (m - base) * C));
+          int row[4];  // of tokens ln, ln + 32, ..
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int s = (m - base) * C + 32 * i + ln;
+            row[i] = s < u.n ? decay_row(a, u, p.mode, u.t0 + s) : -1;
+          }
+          auto go = [&](auto bytes) {
+            constexpr int N = decltype(bytes)::value, PR = D * 2 / N, RW = PR < 32 ? 32 / PR : 1;  // pieces of a row, rows at once
+            const int c = (ln % PR) * (N / 2);
+            const bool any = c < (d + 15) / 16 * 16, in = c < d;  // columns that a product reads; that exist
+            const uint32_t cdst = dst + (c >> 6) * F::ATOM + (N == 16 ? 0u : (c & 4) * 2u);
+            const int ch = (c & 63) >> 3;
+            const char* cb = src0 + 2 * c;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll 2
+              for (int r0 = 0; r0 < 32; r0 += RW) {
+                const int r = r0 + ln / PR;
+                const int gr = __shfl_sync(0xFFFFFFFFu, row[i], r);
+                const bool ok = in && gr >= 0;
+                if (any) cp_piece<N>(cdst + (32 * i + r) * 128 + ((ch ^ (r & 7)) << 4), ok ? cb + gr * st : src0, ok ? N : 0);
+              }
+          };
+          if (wide) go(std::integral_constant<int, 16>{});
+          else go(std::integral_constant<int, 8>{});
+          cp_commit();
+          cp_wait<0>();
+          fence_async_smem();
+          __syncwarp();
+          if (ln == 0) mbar_arrive(&sh.full[x][m & 1]);
+        }
       }
     }
     base = end;
@@ -574,7 +613,10 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       if (ln == 0) mbar_arrive(bar);
     };
 
-    while (next_piece(true)) {
+#pragma unroll 1
+    for (int piece = 0; sh.piece[piece & 1].more; ++piece) {
+    const TcPiece& tab = sh.piece[piece & 1];
+    const DecayPiece& u = tab.u;
     const DecayProblem& p = a.p[same(u.z)];
     const int h = same(u.h);
     // tile row i holds scan position i of the chunk, or 127 - i where a reversed scan's tiles stay in memory order
@@ -586,23 +628,43 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     float S[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) S[j] = 0.f;
+    // S0 and S_final pass through 2 KB of S's shared memory a warp, half of its columns at a time, to 64-byte pieces of rows
+    const uint32_t stage = sb + F::OFF_S + (cg * (D / 32) + (warp & 3)) * 2048;
+    auto state_at = [&](auto* s0, int row, int half) {
+      return reinterpret_cast<std::conditional_t<std::is_const_v<std::remove_pointer_t<decltype(s0)>>, const float4*, float4*>>(
+          s0 + (size_t)(32 * (warp & 3) + row) * p.dv + 32 * cg + 16 * half + 4 * (ln & 3));
+    };
+    auto state_in = [&](int row, int half) { return 32 * (warp & 3) + row < p.dk && 32 * cg + 16 * half + 4 * (ln & 3) < p.dv; };
     // element (c, j) of a block's state: four value channels of consecutive key channels side by side
     auto block_state = [&](int i) { return reinterpret_cast<float4*>(a.segst + (size_t)i * (D * D)) + (cg * 8) * D + t; };
     if (t < D) {
       if (u.t0 == 0 && (STATES || u.last)) {
-        if (p.S0 && u.slot >= 0 && key) {
+        if (p.S0 && u.slot >= 0) {
           const float* s0 = p.S0 + ((size_t)u.slot * a.H + h) * p.dk * p.dv;
           if (p.s0_t) {
+            if (key) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (cg * 32 + j < p.dv) S[j] = s0[(size_t)(cg * 32 + j) * p.dk + t];
+              for (int j = 0; j < 32; ++j)
+                if (cg * 32 + j < p.dv) S[j] = s0[(size_t)(cg * 32 + j) * p.dk + t];
+            }
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              if (cg * 32 + j < p.dv) {
-                const float4 x = *reinterpret_cast<const float4*>(s0 + (size_t)t * p.dv + cg * 32 + j);
-                S[j] = x.x, S[j + 1] = x.y, S[j + 2] = x.z, S[j + 3] = x.w;
+            for (int half = 0; half < 2; ++half) {
+              float4 x[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[i] = state_in(8 * i + ln / 4, half) ? __ldcg(state_at(s0, 8 * i + ln / 4, half)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                sts128(stage + swz_off<64>(8 * i + ln / 4, ln & 3), __float_as_uint(x[i].x), __float_as_uint(x[i].y), __float_as_uint(x[i].z), __float_as_uint(x[i].w));
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint4 v = lds128(stage + swz_off<64>(ln, i));
+                const int j = 16 * half + 4 * i;
+                S[j] = __uint_as_float(v.x), S[j + 1] = __uint_as_float(v.y), S[j + 2] = __uint_as_float(v.z), S[j + 3] = __uint_as_float(v.w);
               }
+              __syncwarp();
+            }
           }
         }
         if (STATES) {  // a copy for the second pass, in which the unit's last block may already have written S_final there
@@ -612,14 +674,12 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         }
       } else if (!STATES) {
         // the states of the blocks that have walked the unit so far; at its start, the copy of S0
-        int j0 = blockIdx.x, j1 = blockIdx.x;
-        const int grid = sh.grid, rem = (int)(sh.grains % grid);
-        if (u.t0 > 0) j0 = (int)(((u.unit_start + 1) * grid - 1) / sh.grains);
-        else j0 = a.deal.grid + blockIdx.x, j1 = j0 + 1;
+        const int j0 = u.t0 > 0 ? tab.j0 : a.deal.grid + blockIdx.x, j1 = u.t0 > 0 ? blockIdx.x : j0 + 1;
+        const unsigned grid = sh.grid, rem = (unsigned)(sh.grains % grid);
 #pragma unroll 2
         for (int i = j0; i < j1; ++i) {
           const float4* ls = block_state(i);
-          const float2 w = sh.step[(int)((long long)(i + 1) * rem / grid - (long long)i * rem / grid) ? kRun1 : kRun];
+          const float2 w = tab.step[(i + 1) * rem / grid != i * rem / grid ? kRun1 : kRun];
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             const float4 x = ls[(j / 4) * D];
@@ -643,7 +703,10 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         }
       }
     };
-    if constexpr (!STATES) put_state();
+    if constexpr (!STATES) {
+      named_bar(9, NT);  // S0 came through the same memory
+      if (left > 0) put_state();
+    }
     // khat^T of chunk m -> tensor memory: the warp's 32 channels, its group's tokens.  LAST: the last of three terms alone,
     // formed again once its place is free (held in registers meanwhile it would push others out to local memory).
     auto convert_k = [&](int m, int terms, auto last) {
@@ -689,7 +752,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     // S = lambda^n S + dS (columns past nv hold nothing that is read)
     auto update = [&](int n, int e) {
       if (32 * (warp & 3) < D) {
-        const float2 w = sh.step[(n < C ? kLast : kFull) + (e ? kFullLag - kFull : 0)];
+        const float2 w = tab.step[(n < C ? kLast : kFull) + (e ? kFullLag - kFull : 0)];
         const uint64_t hi = f2(w.x, w.x), low = f2(w.y, w.y);
         float x[32];
         tmem_take16x2(tmem + lane + F::TM_DS + 32 * cg, tmem + lane + F::TM_DS + 32 * cg + 16, x, x + 16);
@@ -714,11 +777,11 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           float x[16];
           tmem_take16(tmem + lane + F::TM_P + s0, x);
           if (blk != tb) {  // lambda^(t - s) = lambda^(t - s0 - 15) lambda^(15 - i)
-            const float base = p.a * sh.pw[rev ? s0 - t : t - s0 - 15];
+            const float base = p.a * tab.pw[rev ? s0 - t : t - s0 - 15];
             const uint64_t bb = f2(base, base);
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
-              const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&sh.p16[i]);
+              const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&tab.p16[i]);
               f2_out(mul2(mul2(f2(x[i], x[i + 1]), q.x), bb), x[i], x[i + 1]);
               f2_out(mul2(mul2(f2(x[i + 2], x[i + 3]), q.y), bb), x[i + 2], x[i + 3]);
             }
@@ -727,7 +790,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const int k = rev ? i - d : d - i;
-              const float v = x[i] * sh.pa[max(k, 0)];
+              const float v = x[i] * tab.pa[max(k, 0)];
               x[i] = k >= 0 ? v : 0.f;
             }
           }
@@ -748,7 +811,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     auto put_tma = [&](int m, int e) {
       const int jj = 32 * cg;
       if (jj < nv) {
-        const float f = p.c * sh.pw[(rev ? C - 1 - t : t) + 1 - e];
+        const float f = p.c * tab.pw[(rev ? C - 1 - t : t) + 1 - e];
         const uint64_t ff = f2(f, f);
         const uint32_t st = tile(1, m) + (cg >> 1) * F::ATOM;
 #pragma unroll
@@ -795,7 +858,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       const int jj = 32 * cg;
       if (jj >= nv) return;
       const int s = rev ? C - 1 - t : t;
-      const float f = p.c * sh.pw[s + 1 - e];
+      const float f = p.c * tab.pw[s + 1 - e];
       const uint64_t ff = f2(f, f);
       const uint32_t st = tile(1, m) + warp * 2048;
 #pragma unroll
@@ -839,7 +902,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         if (m < end) {
           wait_bar(&sh.full[0][m & 1], (m >> 1) & 1);
           if (__any_sync(0xFFFFFFFFu, timed_out || *reinterpret_cast<volatile int*>(&sh.abort))) break;
-          convert_k(m, terms_of(left - (AHEAD && m > base ? C : 0)), kAll);
+          convert_k(m, terms_of(tab, left - (AHEAD && m > base ? C : 0)), kAll);
         }
         const int j = AHEAD ? m - 1 : m;
         if (!AHEAD) arrive(&sh.bar_k);
@@ -861,14 +924,14 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       auto full = [&](int m) { wait_bar(&sh.full[0][m & 1], (m >> 1) & 1); };
       if (!F::SMALL && left > 0) {
         full(base);
-        convert_k(base, terms_of(left), kAll);
+        convert_k(base, terms_of(tab, left), kAll);
       }
 #pragma unroll 1
       for (int m = base; left > 0; ++m, left -= C) {
         const uint32_t ph = m & 1;
         const int n = min(C, left);
         const int e = (p.lag && u.t0 == 0 && left == u.n) ? 1 : 0;
-        const int terms = terms_of(left);
+        const int terms = terms_of(tab, left);
         if (F::SMALL) full(m);
         // khat (D = 128: its third term) comes over the last chunk's outputs, once the warps of these lanes have read them
         const bool stop = timed_out || *reinterpret_cast<volatile int*>(&sh.abort);
@@ -892,10 +955,10 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         }
         arrive(&sh.bar_p);
         wait_bar(&sh.bar_qs, ph);
-        put_state();
+        if (left > C) put_state();  // (S_final leaves through the same memory)
         if (!F::SMALL && left > C) {  // while the tensor core is at P v
           full(m + 1);
-          convert_k(m + 1, terms_of(left - C), kAll);
+          convert_k(m + 1, terms_of(tab, left - C), kAll);
         }
         wait_bar(&sh.bar_pv, ph);
         tc_fence_after();
@@ -909,13 +972,26 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         if (FETCH == kFetchTokens || left <= C) put_done(m);
       }
       base += same((u.n + C - 1) / C);
-      if (p.Sf && u.slot >= 0 && u.last && key) {
+      if (tab.keep && u.last && 32 * (warp & 3) < D) {
         // dS0 = lambda G_0; an empty sequence passes its state on as it is
-        const float w = p.lag && u.len > 0 ? sh.pw[1] : 1.f;
-        float* out = p.Sf + ((size_t)u.slot * a.H + h) * p.dk * p.dv + (size_t)t * p.dv + cg * 32;
+        const float w = p.lag && u.len > 0 ? tab.pw[1] : 1.f;
+        float* out = p.Sf + ((size_t)u.slot * a.H + h) * p.dk * p.dv;
 #pragma unroll
-        for (int j = 0; j < 32; j += 4)
-          if (cg * 32 + j < p.dv) *reinterpret_cast<float4*>(out + j) = make_float4(w * S[j], w * S[j + 1], w * S[j + 2], w * S[j + 3]);
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = 16 * half + 4 * i;
+            sts128(stage + swz_off<64>(ln, i), __float_as_uint(w * S[j]), __float_as_uint(w * S[j + 1]), __float_as_uint(w * S[j + 2]), __float_as_uint(w * S[j + 3]));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 v = lds128(stage + swz_off<64>(8 * i + ln / 4, ln & 3));
+            if (state_in(8 * i + ln / 4, half))
+              *state_at(out, 8 * i + ln / 4, half) = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+          }
+          __syncwarp();
+        }
       }
     }
     if (!piece_done()) break;
