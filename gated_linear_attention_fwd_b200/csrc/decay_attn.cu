@@ -107,11 +107,11 @@ Deal deal_for(int B, int H, int L, int dk, int dv, bool packed, int nprob) {
   const long long units = (long long)B * H * nprob;
   const int n = packed ? (int)(((long long)L / 128 + B) / (B > 0 ? B : 1)) : (L > 128 ? (L + 127) / 128 : 1);
   const long long total = units * (n > 0 ? n : 1);
-  r.d = DecayDeal{(int)(units < slots ? units : slots), n, n, nprob};
+  r.d = DecayDeal{(int)(units < slots ? units : slots), n, n, nprob, 0, 0};
   const bool cuttable = packed ? L > 128 : n > 1;
   double best = packed && cuttable ? 1e30 : (double)((units + r.d.grid - 1) / r.d.grid) * n;  // packed: dealt by the chunk
   if (cuttable) {
-    for (long long c = (total + slots - 1) / slots, k = 0; c <= n && k < 64; ++c, ++k) {
+    for (long long c = (total + slots - 1) / slots, k = 0; k < 64 && (k == 0 || c <= n); ++c, ++k) {
       const double cost = c + 0.42 * (c < n ? c : n - 1) + 2.0 + 0.1 * ((n + c - 1) / c);
       if (cost < best) {
         best = cost;
@@ -122,6 +122,10 @@ Deal deal_for(int B, int H, int L, int dk, int dv, bool packed, int nprob) {
   }
   if (packed) r.d.gran = 1;
   r.multi = cuttable && r.d.gran == 1;
+  // Six and more blocks to a unit: joining each block's predecessors in the second pass costs some half a microsecond
+  // apiece, a kernel that joins them all once three (2 x 12544 tokens, 6 heads of 32/64: KJOIN).
+  r.d.second = r.multi;
+  r.d.joined = r.multi && !packed && (long long)n * r.d.grid >= 6 * total;
   r.states = r.multi ? (size_t)2 * r.d.grid * r.D * r.D : 0;
   return r;
 }
@@ -172,7 +176,7 @@ void encode_maps(DecayArgs& a, const MapSource* t, int n, const MapSource* o, in
     const uint64_t st = (uint64_t)m.stride, L = (uint64_t)a.L;
     const uint64_t len[2][3] = {{L, a.cu ? 1u : (uint64_t)a.B, 1}, {(uint64_t)a.Hg, (uint64_t)a.Wg, (uint64_t)a.B}};
     const uint64_t stride[2][3] = {{st, L * st, L * st}, {st * (uint64_t)a.Wg, st, L * st}};
-    const uint32_t box = !rows ? kColRun : (i < n ? 128 : kOutRows);
+    const uint32_t box = rows ? 128 : kColRun;
     if (!tmap_heads(i < n ? &a.map[i] : &a.omap[i - n], m.base, m.d, a.H, len[!rows], stride[!rows], box)) return;
   }
   a.fetch = rows ? kFetchRows : kFetchCols;

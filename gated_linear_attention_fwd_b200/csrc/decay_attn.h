@@ -45,12 +45,13 @@ struct DecayDeal {
   int gran;
   int chunks;   // of a unit (without cu)
   int nprob;
+  int second;   // whether a first pass of the same call runs before
+  int joined;   // whether the blocks' states are joined by a kernel of their own
 };
 
 // How the tensor-core kernel fetches tiles: token by token, or by TMA from whole-row or column maps.
 enum { kFetchTokens = 0, kFetchRows = 1, kFetchCols = 2 };
 constexpr int kColRun = 16;  // tokens of a column map's box
-constexpr int kOutRows = 32;  // tokens of a row map's box of an output
 
 struct DecayArgs {
   alignas(64) CUtensorMap map[4];
@@ -175,17 +176,33 @@ struct DecayPiece {
   long long unit_start;  // the unit's first chunk among all units'
 };
 
+// a / b, mostly of small numbers (a 64-bit division is a hundred instructions).
+__host__ __device__ __forceinline__ long long deal_div(long long a, long long b) {
+  return ((a | b) >> 31) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+// `grains` dealt to `grid` blocks: the first `rem` of them take q + 1 each, the others q.
+struct DealRuns {
+  long long q;
+  int rem;
+  __host__ __device__ __forceinline__ DealRuns(long long grains, int grid) : q(deal_div(grains, grid)), rem((int)(grains - q * grid)) {}
+  __device__ __forceinline__ long long start(int i) const { return i * q + min(i, rem); }
+  __device__ __forceinline__ int block_of(long long x) const {
+    const long long head = rem * (q + 1);
+    return (int)(x < head ? deal_div(x, q + 1) : rem + deal_div(x - head, q));
+  }
+};
+
 // The piece that starts at chunk r of all units', `per` of each (problem, head), and ends before chunk r1; one warp.
 __device__ __forceinline__ void decay_piece(const DecayArgs& a, long long per, long long r, long long r1, DecayPiece& u) {
   const int lane = threadIdx.x & 31;
-  const long long zh = r / per;
+  const long long zh = deal_div(r, per);
   const long long w = r - zh * per;
-  u.h = (int)(zh % a.H);
-  u.z = (int)(zh / a.H);
+  u.z = (int)deal_div(zh, a.H);
+  u.h = (int)(zh - (long long)u.z * a.H);
   int nch, c0;
   if (!a.cu) {
     nch = a.deal.chunks;
-    u.b = (int)(w / nch);
+    u.b = (int)deal_div(w, nch);
     c0 = (int)(w - (long long)u.b * nch);
     u.first = u.b * a.L;
     u.len = a.L;

@@ -246,7 +246,9 @@ struct TcPiece {
   DecayPiece u;
   float g;                    // the head's log decay
   int keep;                   // whether the unit's final state is asked for
-  int j0;                     // the block that began the unit
+  int j0;                     // the first block whose state is to be joined
+  int rem;                    // the blocks before this one have the longer runs
+  long long run;              // chunks of the shorter runs
   int more;                   // 0: there is no such piece
 };
 
@@ -258,9 +260,9 @@ struct TcTables {
   uint64_t free_[3][2];             // tile x (k, v, q) of the chunk is no longer read
   uint64_t bar_k, bar_p;            // the workers': khat (with S) written, P written (and dS read)
   uint64_t bar_qk, bar_ds, bar_qs, bar_pv, bar_end;  // the tensor core's
+  uint64_t bar_out[2];              // the outputs of chunk m are staged, m & 1
   // how the chunks are dealt, and what of this block's run is left
-  long long per, grains, at, end;
-  int grid;
+  long long per, at, end;
   uint32_t tmem;
   int abort;
 };
@@ -284,9 +286,11 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     for (int i = 0; i < 2; ++i) {
       for (int x = 0; x < 3; ++x) {
         mbar_init(&sh.full[x][i], 1);
-        mbar_init(&sh.free_[x][i], x == 1 && !STATES ? 4 : 1);
+        mbar_init(&sh.free_[x][i], x == 1 && !STATES && FETCH == kFetchTokens ? NT / 32 : 1);
       }
     }
+    mbar_init(&sh.bar_out[0], NT / 32);
+    mbar_init(&sh.bar_out[1], NT / 32);
     mbar_init(&sh.bar_k, NT / 32);
     mbar_init(&sh.bar_p, NT / 32);
     mbar_init(&sh.bar_qk, 1);
@@ -299,8 +303,16 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     sh.abort = 0;
     fence_mbar_init();
   }
-  griddep_wait();
-  griddep_launch_dependents();
+  // After a first pass (which started after everything before this call had ended) a block plans, fetches its first tiles
+  // and waits for that pass only before it touches states.
+  const bool early = !STATES && FETCH != kFetchTokens && a.deal.second;
+  auto depend = [&]() {
+    griddep_wait();
+    griddep_launch_dependents();
+  };
+  if (!early) depend();
+  if (FETCH != kFetchTokens && warp == W0 + 1 && ln < 7)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(tmap_addr(ln < 4 ? a.map[ln] : a.omap[ln - 4])) : "memory");
   if (!STATES && a.cu && blockIdx.x == 0 && warp == 0) decay_check_offsets(a);
   bool on = true;
   if (sb & 1023u) {  // the swizzled tiles start at 1024-byte boundaries
@@ -322,62 +334,78 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   // Every role walks the pieces, parted by block-wide barriers; one warp plans the next while this one is walked.
   auto plan = [&](int k) {
     TcPiece& t = sh.piece[k & 1];
+    long long per;
+    if (k == 0) per = a.cu ? deal_total(a) : (long long)a.B * a.deal.chunks;
+    else per = sh.per;
+    const long long grains = deal_div(per * a.H * a.deal.nprob, a.deal.gran);
+    const int grid = (int)min((long long)a.deal.grid, grains), me = blockIdx.x;
+    const DealRuns runs(grains, grid);
+    long long r, r1;
     if (k == 0) {
-      const long long per = a.cu ? deal_total(a) : (long long)a.B * a.deal.chunks;
-      const long long grains = per * a.H * a.deal.nprob / a.deal.gran;
-      const int grid = (int)min((long long)a.deal.grid, grains), i = blockIdx.x;
-      if (ln == 0) {
-        sh.per = per;
-        sh.grains = grains;
-        sh.grid = grid;
-        sh.at = on && i < grid ? i * grains / grid * a.deal.gran : 0;
-        sh.end = on && i < grid ? (i + 1) * grains / grid * a.deal.gran : 0;
-      }
-      __syncwarp();
+      r = on && me < grid ? runs.start(me) * a.deal.gran : 0;
+      r1 = on && me < grid ? runs.start(me + 1) * a.deal.gran : 0;
+    } else {
+      r = sh.at;
+      r1 = sh.end;
     }
-    long long r = sh.at;
-    const long long r1 = sh.end;
+    __syncwarp();
     bool more = r < r1;
     if (more) {
       DecayPiece u;
       if (STATES) {  // the last unit's, if it goes on in the next block
-        decay_piece(a, sh.per, r1 - 1, r1, u);
+        decay_piece(a, per, r1 - 1, r1, u);
         r = max(r, u.unit_start);
       }
-      decay_piece(a, sh.per, r, r1, u);
+      decay_piece(a, per, r, r1, u);
       if (STATES) more = !u.last;
-      const DecayProblem& p = a.p[u.z];
-      const float g = a.g[u.h];
       if (ln == 0) {
         t.u = u;
-        t.g = g;
-        t.keep = p.Sf && u.slot >= 0;
-        t.j0 = (int)(((u.unit_start + 1) * sh.grid - 1) / sh.grains);
-        sh.at = STATES ? r1 : r + u.chunks;
+        t.g = a.g[u.h];
+        t.keep = a.p[u.z].Sf && u.slot >= 0;
+        t.j0 = a.deal.joined ? me - 1 : runs.block_of(u.unit_start);
+        t.rem = runs.rem;
+        t.run = runs.q;
       }
-      const bool rev = FETCH != kFetchTokens && (p.mode & 1);
-      const long long run = sh.grains / sh.grid;
-#pragma unroll 1
-      for (int j = ln; j < C + kSteps; j += 32) {
-        // from C on: lambda to the tokens of a whole chunk, of the last one, of either where its first token counts
-        // without its decay (lag), and of the shorter and the longer of the blocks' runs
-        const int last = u.n - max(u.n - 1, 0) / C * C;
-        const long long i = j <= C             ? j
-                            : j == C + kLast    ? last
-                            : j == C + kFullLag ? C - 1
-                            : j == C + kLastLag ? max(last - 1, 0)
-                                                : (run + (j - C - kRun)) * C;
-        const float2 w = decay_pow(g, i);
-        if (j <= C) t.pw[j] = w.x;
-        if (j >= C) t.step[j - C] = w;
-        if (j < 16) t.p16[rev ? j : 15 - j] = w.x;
-        if (j < 32) t.pa[j] = p.a * w.x;
+      if (k > 0 && more && u.t0 == 0 && u.last && a.p[u.z].S0 && u.slot >= 0) {  // on the way to L2 by the time the piece starts
+        const DecayProblem& p = a.p[u.z];
+        const char* s0 = reinterpret_cast<const char*>(p.S0 + ((size_t)u.slot * a.H + u.h) * p.dk * p.dv);
+        for (int i = 128 * ln; i < 4 * p.dk * p.dv; i += 128 * 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(s0 + i));
       }
+      r = STATES ? r1 : r + u.chunks;
     }
-    if (ln == 0) t.more = more;
+    if (ln == 0) {
+      t.more = more;
+      sh.per = per;
+      sh.at = r;
+      sh.end = r1;
+    }
     __syncwarp();
   };
+  // The powers of a piece, by `step` threads.
+  auto powers = [&](TcPiece& t, int first, int step) {
+    if (!t.more) return;
+    const DecayProblem& p = a.p[t.u.z];
+    const bool rev = FETCH != kFetchTokens && (p.mode & 1);
+#pragma unroll 1
+    for (int j = first; j < C + kSteps; j += step) {
+      // from C on: lambda to the tokens of a whole chunk, of the last one, of either where its first token counts
+      // without its decay (lag), and of the shorter and the longer of the blocks' runs
+      const int last = t.u.n - max(t.u.n - 1, 0) / C * C;
+      const long long i = j <= C             ? j
+                          : j == C + kLast    ? last
+                          : j == C + kFullLag ? C - 1
+                          : j == C + kLastLag ? max(last - 1, 0)
+                                              : (t.run + (j - C - kRun)) * C;
+      const float2 w = decay_pow(t.g, i);
+      if (j <= C) t.pw[j] = w.x;
+      if (j >= C) t.step[j - C] = w;
+      if (j < 16) t.p16[rev ? j : 15 - j] = w.x;
+      if (j < 32) t.pa[j] = p.a * w.x;
+    }
+  };
   if (warp == W0 + 3) plan(0);
+  __syncthreads();
+  if (tid < NT) powers(sh.piece[0], tid, NT);
   __syncthreads();
   // Every role is through with the piece; false: one gave up.
   auto piece_done = [&]() {
@@ -397,6 +425,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   if (warp == W0) {
     // ---- the issuing warp
     regs_down<F::SERVICE_REGS>();
+    if (early) depend();
     const uint32_t one = elect_one();
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
 #pragma unroll 1
@@ -474,6 +503,8 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     // ---- the fetching warps
     regs_down<F::SERVICE_REGS>();
     uint32_t cleaned = 0;  // pieces whose last tiles were cleaned
+    bool due = early;      // to wait for the first pass: the fetching warp first asks for two chunks
+    if (early && warp != W0 + 1) depend();
 #pragma unroll 1
     for (int piece = 0; sh.piece[piece & 1].more; ++piece) {
     const TcPiece& tab = sh.piece[piece & 1];
@@ -481,7 +512,11 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     const DecayProblem& p = a.p[same(u.z)];
     const int h = same(u.h), end = base + same((u.n + C - 1) / C);
     const bool rev = FETCH != kFetchTokens && (p.mode & 1);
-    if (warp == W0 + 3) plan(piece + 1);
+    if (warp == W0 + 3) {
+      plan(piece + 1);
+      powers(sh.piece[(piece + 1) & 1], ln, 32);
+      __syncwarp();
+    }
     // the weights of khat in chunk m of n tokens
     auto weights = [&](int m, int n) {
 #pragma unroll
@@ -495,7 +530,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       return m < 2 || __all_sync(0xFFFFFFFFu, wait_bar(&sh.free_[x][m & 1], ((m - 2) >> 1) & 1));
     };
     if constexpr (FETCH != kFetchTokens) {
-      // one warp asks for a chunk's tiles in the order in which their places become free
+      // one warp asks for a chunk's tiles in the order in which their places become free, one stores outputs, one plans
       if (warp == W0 + 1) {
         auto fetch = [&](int x, int m, bool clean) {
           const uint32_t dst = tile(x, m);
@@ -526,6 +561,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           const int n = min(C, u.n - (m - base) * C);
           // packed: rows past the sequence's end are another's, and 0 times them need not be 0
           const bool clean = a.cu && n < C;
+          if (due && m == 2) depend(), due = false;
           if (!freed(0, m)) break;
           weights(m, n);
           fetch(0, m, clean);
@@ -549,6 +585,37 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
             }
             ++cleaned;
           }
+        }
+      }
+      if (!STATES && warp == W0 + 2) {
+        // whole chunks' outputs, from where the workers staged them (over the v tile, in its layout)
+        const CUtensorMap& map = a.omap[same(u.z)];
+        const int atoms = (p.dv + 63) / 64;
+#pragma unroll 1
+        for (int m = base; m < end; ++m) {
+          if (!__all_sync(0xFFFFFFFFu, wait_bar(&sh.bar_out[m & 1], (m >> 1) & 1))) break;
+          const int t0 = u.t0 + (m - base) * C;
+          if (ln == 0) {
+            if (u.n - (m - base) * C >= C) {
+              const uint32_t src = tile(1, m);
+              if constexpr (FETCH == kFetchRows) {
+                const int r = (rev ? u.len - t0 - C : t0) + (a.cu ? u.first : 0);
+                for (int i = 0; i < atoms; ++i) tma_store_5d(map, 64 * i, h, r, a.cu ? 0 : u.b, 0, src + i * F::ATOM);
+              } else {
+                const int f0 = rev ? a.L - t0 - C : t0;
+                int col = f0 / a.Hg, y = f0 - col * a.Hg;
+                for (int r = 0; r < C; r += kColRun) {
+                  for (int i = 0; i < atoms; ++i) tma_store_5d(map, 64 * i, h, y, col, u.b, src + i * F::ATOM + r * 128);
+                  y += kColRun;
+                  if (y >= a.Hg) y = 0, ++col;
+                }
+              }
+              bulk_commit();
+              bulk_wait_read_all();
+            }
+            mbar_arrive(&sh.free_[1][m & 1]);
+          }
+          __syncwarp();
         }
       }
     } else {
@@ -601,6 +668,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     base = end;
     if (!piece_done()) break;
     }
+    if (!STATES && FETCH != kFetchTokens && warp == W0 + 2) bulk_wait_all();  // no store outlives the block
   } else {
     // ---- the workers
     regs_up<F::WORKER_REGS>();
@@ -620,6 +688,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     const DecayProblem& p = a.p[same(u.z)];
     const int h = same(u.h);
     // tile row i holds scan position i of the chunk, or 127 - i where a reversed scan's tiles stay in memory order
+    if (early && piece == 0) depend();
     const bool rev = FETCH != kFetchTokens && (p.mode & 1);
     const int kk = (p.dk + 15) / 16;                // K-steps over the key channels
     const int nv = (p.dv + 15) / 16 * 16;           // columns of the products with v or S
@@ -675,11 +744,10 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       } else if (!STATES) {
         // the states of the blocks that have walked the unit so far; at its start, the copy of S0
         const int j0 = u.t0 > 0 ? tab.j0 : a.deal.grid + blockIdx.x, j1 = u.t0 > 0 ? blockIdx.x : j0 + 1;
-        const unsigned grid = sh.grid, rem = (unsigned)(sh.grains % grid);
 #pragma unroll 2
         for (int i = j0; i < j1; ++i) {
           const float4* ls = block_state(i);
-          const float2 w = tab.step[(i + 1) * rem / grid != i * rem / grid ? kRun1 : kRun];
+          const float2 w = tab.step[i < tab.rem ? kRun1 : kRun];
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             const float4 x = ls[(j / 4) * D];
@@ -805,9 +873,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       }
       tmem_st_wait();
     };
-    // The output rows of a whole chunk: staged over the v tile, in its layout, and stored by TMA, 32 rows at a time (one
-    // thread of the warps of these lanes; it lets go of the tile later, in put_done).
-    const bool storer = warp < 4 && ln == 0;
+    // The output rows of a whole chunk, staged over the v tile in its layout for a TMA store
     auto put_tma = [&](int m, int e) {
       const int jj = 32 * cg;
       if (jj < nv) {
@@ -826,32 +892,6 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           sts128(st + swz_off<128>(t, ch + 1), w[4], w[5], w[6], w[7]);
         }
       }
-      fence_async_smem();
-      named_bar(5 + (warp & 3), 32 * CG);
-      if (storer) {
-        const CUtensorMap& map = a.omap[u.z];
-        const uint32_t src = tile(1, m) + warp * 4096;
-        const int atoms = (p.dv + 63) / 64, t0 = u.t0 + u.n - left, i0 = 32 * warp;
-        if constexpr (FETCH == kFetchRows) {
-          const int r = (rev ? u.len - t0 - C : t0) + i0 + (a.cu ? u.first : 0);
-          for (int i = 0; i < atoms; ++i) tma_store_5d(map, 64 * i, h, r, a.cu ? 0 : u.b, 0, src + i * F::ATOM);
-        } else {
-          const int f0 = (rev ? a.L - t0 - C : t0) + i0;
-          int col = f0 / a.Hg, y = f0 - col * a.Hg;
-          for (int r = 0; r < 32; r += kColRun) {
-            for (int i = 0; i < atoms; ++i) tma_store_5d(map, 64 * i, h, y, col, u.b, src + i * F::ATOM + r * 128);
-            y += kColRun;
-            if (y >= a.Hg) y = 0, ++col;
-          }
-        }
-        bulk_commit();
-      }
-    };
-    // The tile that chunk m's outputs were staged in may be fetched over.
-    auto put_done = [&](int m) {
-      if (FETCH != kFetchTokens && storer) bulk_wait_read_all();
-      __syncwarp();
-      if (storer) mbar_arrive(&sh.free_[1][m & 1]);
     };
     // The same of any chunk: the warp's 32 rows x 32 columns through its 2 KB of the v tile, to 64-byte pieces of rows
     auto put_out = [&](int m, int e) {
@@ -944,7 +984,6 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           tc_fence_after();
           convert_p();
         }
-        if (FETCH != kFetchTokens && left != u.n) put_done(m - 1);
         wait_bar(&sh.bar_ds, ph);
         tc_fence_after();
         update(n, e);  // before P v, which comes to stand in dS's place
@@ -962,14 +1001,9 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         }
         wait_bar(&sh.bar_pv, ph);
         tc_fence_after();
-        if (FETCH != kFetchTokens && n == C) {
-          put_tma(m, e);
-        } else {
-          put_out(m, e);
-          fence_async_smem();  // the next tile comes over what was staged there
-          named_bar(5 + (warp & 3), 32 * CG);
-        }
-        if (FETCH == kFetchTokens || left <= C) put_done(m);
+        if (FETCH != kFetchTokens && n == C) put_tma(m, e);
+        else put_out(m, e);
+        arrive(FETCH != kFetchTokens ? &sh.bar_out[m & 1] : &sh.free_[1][m & 1]);  // (the tile is stored from, or fetched over)
       }
       base += same((u.n + C - 1) / C);
       if (tab.keep && u.last && 32 * (warp & 3) < D) {
@@ -996,13 +1030,45 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     }
     if (!piece_done()) break;
     }
-    if (!STATES && FETCH != kFetchTokens && warp < 4) bulk_wait_all();
   }
   if (timed_out) set_status(a.status, DIG_ERR_DEVICE_TIMEOUT);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == W0) tmem_dealloc(tmem, F::TM_COLS);
+}
+
+// The states that the first pass left, joined in place: block i's then is its unit's state up to the end of its run.
+template <int D>
+__global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__ DecayArgs a) {
+  __shared__ float2 step[2];
+  griddep_wait();
+  griddep_launch_dependents();
+  const long long per = (long long)a.B * a.deal.chunks, start = (long long)blockIdx.x * a.deal.chunks;
+  const DealRuns runs(per * a.H * a.deal.nprob, a.deal.grid);
+  const int j0 = runs.block_of(start), j1 = runs.block_of(start + a.deal.chunks - 1);  // the last one's is not needed
+  const long long zh = deal_div(blockIdx.x, a.B);
+  if (threadIdx.x < 2) step[threadIdx.x] = decay_pow(a.g[zh % a.H], (runs.q + threadIdx.x) * C);
+  __syncthreads();
+  float4* s = reinterpret_cast<float4*>(a.segst) + blockIdx.y * 256 + threadIdx.x;
+  constexpr int STATE = D * D / 4;
+  if (j1 - j0 < 2) return;
+  float4 S = s[(size_t)j0 * STATE];
+  for (int i0 = j0 + 1; i0 < j1; i0 += 8) {
+    float4 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = s[(size_t)min(i0 + i, j1 - 1) * STATE];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i0 + i < j1) {
+        const float2 w = step[i0 + i < runs.rem];
+        S.x = fmaf(w.x, S.x, fmaf(w.y, S.x, x[i].x));
+        S.y = fmaf(w.x, S.y, fmaf(w.y, S.y, x[i].y));
+        S.z = fmaf(w.x, S.z, fmaf(w.y, S.z, x[i].z));
+        S.w = fmaf(w.x, S.w, fmaf(w.y, S.w, x[i].w));
+        s[(size_t)(i0 + i) * STATE] = S;
+      }
+  }
 }
 
 template <int D, bool STATES, int FETCH>
@@ -1018,6 +1084,9 @@ template <int D, int FETCH>
 cudaError_t passes(const DecayArgs& a, bool multi, cudaStream_t s) {
   cudaError_t e;
   if (multi && (e = run<D, true, FETCH>(a, s)) != cudaSuccess) return e;
+  if (multi && a.deal.joined &&
+      (e = launch_pdl(decay_join_kernel<D>, dim3(a.B * a.H * a.deal.nprob, D * D / 1024), dim3(256), 0, s, a)) != cudaSuccess)
+    return e;
   return run<D, false, FETCH>(a, s);
 }
 
