@@ -15,6 +15,9 @@ void set_last_error(const char* msg);       // dig_api.cu
 namespace {
 
 constexpr int kSms = 148;
+// The workspace: header, the blocks' flags (in one place for every call that uses it, since calls leave them zero), states.
+constexpr size_t kWsStates = 2048;
+static_assert(sizeof(WsHeader) + 2 * kSms * sizeof(uint32_t) <= kWsStates, "a flag for each block");
 
 struct Cut {
   int D;          // the kernels' padded head dim
@@ -107,7 +110,7 @@ Deal deal_for(int B, int H, int L, int dk, int dv, bool packed, int nprob) {
   const long long units = (long long)B * H * nprob;
   const int n = packed ? (int)(((long long)L / 128 + B) / (B > 0 ? B : 1)) : (L > 128 ? (L + 127) / 128 : 1);
   const long long total = units * (n > 0 ? n : 1);
-  r.d = DecayDeal{(int)(units < slots ? units : slots), n, n, nprob, 0, 0};
+  r.d = DecayDeal{(int)(units < slots ? units : slots), n, n, nprob, 0, 0, 0};
   const bool cuttable = packed ? L > 128 : n > 1;
   double best = packed && cuttable ? 1e30 : (double)((units + r.d.grid - 1) / r.d.grid) * n;  // packed: dealt by the chunk
   if (cuttable) {
@@ -121,12 +124,18 @@ Deal deal_for(int B, int H, int L, int dk, int dv, bool packed, int nprob) {
     }
   }
   if (packed) r.d.gran = 1;
-  r.multi = cuttable && r.d.gran == 1;
+  // units no longer than a run, so that each is cut once at most: one pass, the state handed from block to block
+  if (!packed && cuttable && deal_div(total, slots) >= n && (double)((total + slots - 1) / slots) + 1.0 < best) {
+    r.d.grid = (int)slots;
+    r.d.gran = 1;
+    r.d.handoff = 1;
+  }
+  r.multi = cuttable && r.d.gran == 1 && !r.d.handoff;
   // Six and more blocks to a unit: joining each block's predecessors in the second pass costs some half a microsecond
   // apiece, a kernel that joins them all once three (2 x 12544 tokens, 6 heads of 32/64: KJOIN).
   r.d.second = r.multi;
   r.d.joined = r.multi && !packed && (long long)n * r.d.grid >= 6 * total;
-  r.states = r.multi ? (size_t)2 * r.d.grid * r.D * r.D : 0;
+  r.states = r.d.handoff ? (size_t)r.d.grid * r.D * r.D : r.multi ? (size_t)2 * r.d.grid * r.D * r.D : 0;
   return r;
 }
 
@@ -183,12 +192,14 @@ void encode_maps(DecayArgs& a, const MapSource* t, int n, const MapSource* o, in
 }
 
 dig_status launch(DecayArgs& a, int nprob, int dk, int dv, void* ws, int dtype, int out_dtype, cudaStream_t s) {
-  a.segst = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sizeof(WsHeader));
+  a.segst = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsStates);
   a.status = &static_cast<WsHeader*>(ws)->status;
   cudaError_t e;
   if (on_tc(dtype, out_dtype)) {
     const Deal d = deal_for(a.B, a.H, a.L, dk, dv, a.cu != nullptr, nprob);
     a.deal = d.d;
+    a.flag = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + sizeof(WsHeader));
+    a.counter = static_cast<WsHeader*>(ws)->pad;
     e = launch_decay_tc(a, d.multi, d.D, s);
   } else {
     const Cut c = cut_for(a.B, a.H, a.L, dk, dv, a.cu != nullptr, nprob);
@@ -216,7 +227,7 @@ size_t dig_decay_attn_workspace_bytes(int B, int H, int L, int d_k, int d_v, int
     const size_t m = deal_for(B, H, L, d_k, d_v, packed != 0, pass ? 3 : 1).states;
     n = m > n ? m : n;
   }
-  return sizeof(WsHeader) + n * sizeof(float);
+  return kWsStates + n * sizeof(float);
 }
 
 dig_status dig_decay_attn_fwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,

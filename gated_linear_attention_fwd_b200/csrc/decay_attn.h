@@ -46,6 +46,10 @@ struct DecayDeal {
   int chunks;   // of a unit (without cu)
   int nprob;
   int second;   // whether a first pass of the same call runs before
+  // Whether a block hands the state at its run's end to the next one (units no longer than a run): it walks the beginning
+  // of its last unit first and the end of its first unit last, so that the state is there long before it is asked for.
+  // Blocks are numbered as they start, and wait only for lower numbers.
+  int handoff;
   int joined;   // whether the blocks' states are joined by a kernel of their own
 };
 
@@ -66,6 +70,8 @@ struct DecayArgs {
   int seg;        // tokens of a segment
   int nps;        // segments of a sequence of L tokens (without cu)
   DecayDeal deal;
+  uint32_t* flag;     // [block] a block's state has been handed over (left zero)
+  uint32_t* counter;  // blocks started, blocks done (left zero)
   float* segst;   // tensor core: [2][block][D * D], a block's unfinished unit's state and the copy of its S0; else [problem][segment][H][D * D] segment states
   long long segst_problem;  // elements between problems there
   uint32_t* status;

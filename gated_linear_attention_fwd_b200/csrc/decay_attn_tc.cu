@@ -262,7 +262,8 @@ struct TcTables {
   uint64_t bar_qk, bar_ds, bar_qs, bar_pv, bar_end;  // the tensor core's
   uint64_t bar_out[2];              // the outputs of chunk m are staged, m & 1
   // how the chunks are dealt, and what of this block's run is left
-  long long per, at, end;
+  long long per, at, end, first, first_end;
+  int me;                           // this block's number
   uint32_t tmem;
   int abort;
 };
@@ -338,16 +339,35 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     if (k == 0) per = a.cu ? deal_total(a) : (long long)a.B * a.deal.chunks;
     else per = sh.per;
     const long long grains = deal_div(per * a.H * a.deal.nprob, a.deal.gran);
-    const int grid = (int)min((long long)a.deal.grid, grains), me = blockIdx.x;
+    const int grid = (int)min((long long)a.deal.grid, grains);
     const DealRuns runs(grains, grid);
-    long long r, r1;
+    long long r, r1, first, first_end;  // the next piece's start, the last's end; a piece left for last
+    int me = blockIdx.x;
     if (k == 0) {
+      if (a.deal.handoff) {
+        if (ln == 0) me = (int)atomicAdd(a.counter, 1u);
+        me = __shfl_sync(0xFFFFFFFFu, me, 0);
+      }
       r = on && me < grid ? runs.start(me) * a.deal.gran : 0;
       r1 = on && me < grid ? runs.start(me + 1) * a.deal.gran : 0;
+      first = first_end = 0;
+      if (a.deal.handoff && r < r1) {  // the end of the run's first unit comes last
+        const long long n = a.deal.chunks;
+        first = r;
+        first_end = r = deal_div(r + n - 1, n) * n;
+      }
     } else {
+      me = sh.me;
       r = sh.at;
       r1 = sh.end;
+      first = sh.first;
+      first_end = sh.first_end;
     }
+    // the beginning of the run's last unit comes first: [r1 - tail, r1)
+    const bool tail_first = k == 0 && a.deal.handoff && r1 % a.deal.chunks != 0;
+    const long long next = r, next_end = tail_first ? deal_div(r1, a.deal.chunks) * a.deal.chunks : r1;
+    if (tail_first) r = next_end;
+    else if (a.deal.handoff && r >= r1) r = first, r1 = first_end, first = first_end;
     __syncwarp();
     bool more = r < r1;
     if (more) {
@@ -362,7 +382,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         t.u = u;
         t.g = a.g[u.h];
         t.keep = a.p[u.z].Sf && u.slot >= 0;
-        t.j0 = a.deal.joined ? me - 1 : runs.block_of(u.unit_start);
+        t.j0 = a.deal.joined || a.deal.handoff ? me - 1 : runs.block_of(u.unit_start);
         t.rem = runs.rem;
         t.run = runs.q;
       }
@@ -371,13 +391,16 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         const char* s0 = reinterpret_cast<const char*>(p.S0 + ((size_t)u.slot * a.H + u.h) * p.dk * p.dv);
         for (int i = 128 * ln; i < 4 * p.dk * p.dv; i += 128 * 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(s0 + i));
       }
-      r = STATES ? r1 : r + u.chunks;
+      r = STATES ? r1 : tail_first ? next : r + u.chunks;
     }
     if (ln == 0) {
       t.more = more;
       sh.per = per;
       sh.at = r;
-      sh.end = r1;
+      sh.end = tail_first ? next_end : r1;
+      sh.first = first;
+      sh.first_end = first_end;
+      sh.me = me;
     }
     __syncwarp();
   };
@@ -419,6 +442,21 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   auto terms_of = [&](const TcPiece& t, int left) {
     const int after = t.u.len - t.u.t0 - t.u.n + left - C;  // tokens of the sequence after the chunk
     return same(t.keep && t.g * max(after, 0) >= -7.f ? 3 : 2);
+  };
+  // Waits, as long as wait_bar would, for another block's flag.
+  auto wait_flag = [&](const uint32_t* f) {
+    uint64_t t0 = 0;
+    while (true) {
+      uint32_t v;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(f) : "memory");
+      if (v || timed_out || *reinterpret_cast<volatile int*>(&sh.abort)) return;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kSpinLimitNs) {
+        timed_out = true;
+        sh.abort = 1;
+      }
+    }
   };
   int base = 0;  // chunks before this piece: they are counted through the pieces
 
@@ -694,6 +732,10 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     const int nv = (p.dv + 15) / 16 * 16;           // columns of the products with v or S
     const bool key = t < D && t < p.dk;             // this lane holds a key channel of the state
     // ---- the state the piece starts from: lane t = key channel, value channels 32 cg ..
+    if (!STATES && a.deal.handoff && u.t0 > 0) {  // the state of the block before
+      if (ln == 0) wait_flag(a.flag + sh.me - 1);
+      __syncwarp();
+    }
     float S[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) S[j] = 0.f;
@@ -707,7 +749,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     // element (c, j) of a block's state: four value channels of consecutive key channels side by side
     auto block_state = [&](int i) { return reinterpret_cast<float4*>(a.segst + (size_t)i * (D * D)) + (cg * 8) * D + t; };
     if (t < D) {
-      if (u.t0 == 0 && (STATES || u.last)) {
+      if (u.t0 == 0 && (STATES || u.last || a.deal.handoff)) {
         if (p.S0 && u.slot >= 0) {
           const float* s0 = p.S0 + ((size_t)u.slot * a.H + h) * p.dk * p.dv;
           if (p.s0_t) {
@@ -743,14 +785,14 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         }
       } else if (!STATES) {
         // the states of the blocks that have walked the unit so far; at its start, the copy of S0
-        const int j0 = u.t0 > 0 ? tab.j0 : a.deal.grid + blockIdx.x, j1 = u.t0 > 0 ? blockIdx.x : j0 + 1;
+        const int j0 = u.t0 > 0 ? tab.j0 : a.deal.grid + blockIdx.x, j1 = u.t0 > 0 ? sh.me : j0 + 1;
 #pragma unroll 2
         for (int i = j0; i < j1; ++i) {
           const float4* ls = block_state(i);
           const float2 w = tab.step[i < tab.rem ? kRun1 : kRun];
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            const float4 x = ls[(j / 4) * D];
+            const float4 x = __ldcg(ls + (j / 4) * D);
             S[j] = fmaf(w.x, S[j], fmaf(w.y, S[j], x.x));
             S[j + 1] = fmaf(w.x, S[j + 1], fmaf(w.y, S[j + 1], x.y));
             S[j + 2] = fmaf(w.x, S[j + 2], fmaf(w.y, S[j + 2], x.z));
@@ -1006,6 +1048,17 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         arrive(FETCH != kFetchTokens ? &sh.bar_out[m & 1] : &sh.free_[1][m & 1]);  // (the tile is stored from, or fetched over)
       }
       base += same((u.n + C - 1) / C);
+      if (a.deal.handoff && !u.last) {  // to the next block
+        if (t < D) {
+          float4* out = block_state(sh.me);
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) out[(j / 4) * D] = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+        }
+        __threadfence();
+        named_bar(9, NT);
+        if (tid == 0) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(a.flag + sh.me), "r"(1u) : "memory");
+      }
+      if (a.deal.handoff && u.t0 > 0 && tid == 0) a.flag[sh.me - 1] = 0u;  // every warp has seen it: all are past this unit's chunks
       if (tab.keep && u.last && 32 * (warp & 3) < D) {
         // dS0 = lambda G_0; an empty sequence passes its state on as it is
         const float w = p.lag && u.len > 0 ? tab.pw[1] : 1.f;
@@ -1036,6 +1089,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   __syncthreads();
   tc_fence_after();
   if (warp == W0) tmem_dealloc(tmem, F::TM_COLS);
+  if (a.deal.handoff && tid == 0 && atomicAdd(a.counter + 1, 1u) == gridDim.x - 1) a.counter[0] = a.counter[1] = 0u;
 }
 
 // The states that the first pass left, joined in place: block i's then is its unit's state up to the end of its run.
