@@ -677,20 +677,18 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
             row[i] = s < u.n ? decay_row(a, u, p.mode, u.t0 + s) : -1;
           }
           auto go = [&](auto bytes) {
-            constexpr int N = decltype(bytes)::value, PR = D * 2 / N, RW = PR < 32 ? 32 / PR : 1;  // pieces of a row, rows at once
-            const int c = (ln % PR) * (N / 2);
-            const bool any = c < (d + 15) / 16 * 16, in = c < d;  // columns that a product reads; that exist
-            const uint32_t cdst = dst + (c >> 6) * F::ATOM + (N == 16 ? 0u : (c & 4) * 2u);
-            const int ch = (c & 63) >> 3;
-            const char* cb = src0 + 2 * c;
+            constexpr int N = decltype(bytes)::value;
+            const int pieces = (d + 15) / 16 * 32 / N;  // of a row: the columns that a product reads
+            const int inv = (65536 + pieces - 1) / pieces;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-#pragma unroll 2
-              for (int r0 = 0; r0 < 32; r0 += RW) {
-                const int r = r0 + ln / PR;
+#pragma unroll 4
+              for (int at = ln; at < 32 * pieces; at += 32) {
+                const int r = (at * inv) >> 16, c = (at - r * pieces) * (N / 2), rr = 32 * i + r;
                 const int gr = __shfl_sync(0xFFFFFFFFu, row[i], r);
-                const bool ok = in && gr >= 0;
-                if (any) cp_piece<N>(cdst + (32 * i + r) * 128 + ((ch ^ (r & 7)) << 4), ok ? cb + gr * st : src0, ok ? N : 0);
+                const bool ok = c < d && gr >= 0;
+                const uint32_t to = dst + (c >> 6) * F::ATOM + rr * 128 + ((((c & 63) >> 3) ^ (rr & 7)) << 4) + (N == 16 ? 0 : (c & 4) * 2);
+                cp_piece<N>(to, ok ? src0 + gr * st + 2 * c : src0, ok ? N : 0);
               }
           };
           if (wide) go(std::integral_constant<int, 16>{});
