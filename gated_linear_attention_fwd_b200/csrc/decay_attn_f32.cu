@@ -87,16 +87,25 @@ __global__ void __launch_bounds__(256) decay_f32_kernel(const __grid_constant__ 
 #pragma unroll
       for (int i = 0; i < TC; ++i)
 #pragma unroll
-        for (int j = 0; j < TC; ++j) S[i][j] = s0[(c0 + i) * D + jcol(j)];
+        for (int j = 0; j < TC; j += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(s0 + (c0 + i) * D + jcol(j));
+          S[i][j] = x.x, S[i][j + 1] = x.y, S[i][j + 2] = x.z, S[i][j + 3] = x.w;
+        }
     } else {
       const float2 w = decay_pow(g, a.seg);
+#pragma unroll (TC == 4 ? 4 : 1)
       for (int m = 0; m < u.i; ++m) {
         const float* ls = seg_state(seg0 + m);
 #pragma unroll
         for (int i = 0; i < TC; ++i)
 #pragma unroll
-          for (int j = 0; j < TC; ++j)
-            S[i][j] = fmaf(w.x, S[i][j], fmaf(w.y, S[i][j], ls[(c0 + i) * D + jcol(j)]));
+          for (int j = 0; j < TC; j += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(ls + (c0 + i) * D + jcol(j));
+            S[i][j] = fmaf(w.x, S[i][j], fmaf(w.y, S[i][j], x.x));
+            S[i][j + 1] = fmaf(w.x, S[i][j + 1], fmaf(w.y, S[i][j + 1], x.y));
+            S[i][j + 2] = fmaf(w.x, S[i][j + 2], fmaf(w.y, S[i][j + 2], x.z));
+            S[i][j + 3] = fmaf(w.x, S[i][j + 3], fmaf(w.y, S[i][j + 3], x.w));
+          }
       }
     }
   }
@@ -105,7 +114,8 @@ __global__ void __launch_bounds__(256) decay_f32_kernel(const __grid_constant__ 
 #pragma unroll
     for (int i = 0; i < TC; ++i)
 #pragma unroll
-      for (int j = 0; j < TC; ++j) s0[(c0 + i) * D + jcol(j)] = S[i][j];
+      for (int j = 0; j < TC; j += 4)
+        *reinterpret_cast<float4*>(s0 + (c0 + i) * D + jcol(j)) = make_float4(S[i][j], S[i][j + 1], S[i][j + 2], S[i][j + 3]);
   }
   const T* q = static_cast<const T*>(p.q) + (size_t)h * p.dk;
   const T* k = static_cast<const T*>(p.k) + (size_t)h * p.dk;

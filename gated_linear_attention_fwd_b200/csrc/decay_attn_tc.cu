@@ -11,7 +11,7 @@
 // warp issues them, three more fetch a tile each, and the rest (4 warps per 32
 // lanes at D = 128, 2 at D = 64, so that a thread holds 32 columns of S, dS and O
 // either way) do what is between the products:
-//   - q, k, v tiles (raw bf16, exact) come two chunks deep into 128-byte-swizzled
+//   - q, k, v tiles (raw bf16, exact) come two chunks deep (three in the first pass) into 128-byte-swizzled
 //     tiles of 64 channels, by TMA (boxes of whole rows, or of runs of a grid
 //     column; a reversed scan keeps its tiles in memory order and mirrors the mask)
 //     or, where alignment or the grid does not allow that, token by token through
@@ -36,6 +36,9 @@
 // At D = 128 khat of the next chunk is formed while P v runs, and q k^T of the next
 // chunk follows P v at once.
 #include <cuda_bf16.h>
+
+#include <atomic>
+#include <type_traits>
 
 #include "decay_attn.h"
 #include "sm100.cuh"
@@ -219,8 +222,9 @@ struct TcCfg {
   static constexpr int TILE = ATOM * (D / 64);
   static constexpr int PER = STATES ? 2 : 3;      // tiles of a chunk: k, v, q
   static constexpr int S_ATOM = D * 128;
-  static constexpr int OFF_S = PER * 2 * TILE;
-  static constexpr int OFF_T = OFF_S + S_ATOM * (D / 64);
+  static constexpr int ST = STATES ? 3 : 2;       // chunks in shared memory
+  static constexpr int OFF_S = PER * ST * TILE;
+  static constexpr int OFF_T = OFF_S + (STATES ? 0 : S_ATOM * (D / 64));
   // Registers: 512 x 104 + 128 x 56 of 640 x 96 (D = 128), 256 x 96 + 128 x 48 of 384 x 80 (D = 64).  What does not fit goes
   // to local memory, for which little L1 is left beside the tiles: a load from there costs a trip to L2.
   static constexpr int WORKER_REGS = SMALL ? 96 : 104, SERVICE_REGS = SMALL ? 48 : 56;
@@ -252,12 +256,13 @@ struct TcPiece {
   int more;                   // 0: there is no such piece
 };
 
+template <int ST>
 struct TcTables {
   TcPiece piece[2];
-  float wk[2][C];                   // b lambda^(n-1-s) of chunk m in m & 1, 0 past its end
-  uint64_t full[3][2];              // tile x (k, v, q) of the chunk has come
+  float wk[ST][C];                  // b lambda^(n-1-s) of chunk m in m % ST, 0 past its end
+  uint64_t full[3][ST];             // tile x (k, v, q) of the chunk has come
   uint64_t landed[2];               // k and v of a chunk that ends inside its tiles
-  uint64_t free_[3][2];             // tile x (k, v, q) of the chunk is no longer read
+  uint64_t free_[3][ST];            // tile x (k, v, q) of the chunk is no longer read
   uint64_t bar_k, bar_p;            // the workers': khat (with S) written, P written (and dS read)
   uint64_t bar_qk, bar_ds, bar_qs, bar_pv, bar_end;  // the tensor core's
   uint64_t bar_out[2];              // the outputs of chunk m are staged, m & 1
@@ -273,10 +278,11 @@ struct TcTables {
 template <int D, bool STATES, int FETCH>
 __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) decay_tc_kernel(const __grid_constant__ DecayArgs a) {
   using F = TcCfg<D, STATES>;
-  static_assert(F::OFF_T + sizeof(TcTables) <= (D == 64 ? 113 : 227) * 1024, "the blocks of an SM fit its shared memory");
+  static_assert(F::OFF_T + sizeof(TcTables<F::ST>) <= (D == 64 ? 113 : 227) * 1024, "the blocks of an SM fit its shared memory");
   constexpr int NT = F::NT, CG = F::CG, W0 = NT / 32;
   extern __shared__ __align__(1024) uint8_t smem[];
-  TcTables& sh = *reinterpret_cast<TcTables*>(smem + F::OFF_T);
+  using Tables = TcTables<F::ST>;
+  Tables& sh = *reinterpret_cast<Tables*>(smem + F::OFF_T);
   const int tid = threadIdx.x, warp = tid >> 5, ln = tid & 31;
   const uint32_t sb = smem_u32(smem);
   if (warp == W0) {
@@ -284,7 +290,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < F::ST; ++i) {
       for (int x = 0; x < 3; ++x) {
         mbar_init(&sh.full[x][i], 1);
         mbar_init(&sh.free_[x][i], x == 1 && !STATES && FETCH == kFetchTokens ? NT / 32 : 1);
@@ -435,7 +441,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     named_bar(0, NT + 128);
     return *reinterpret_cast<volatile int*>(&sh.abort) == 0;
   };
-  auto tile = [&](int x, int m) { return sb + ((m & 1) * F::PER + x) * F::TILE; };  // x: 0 k, 1 v, 2 q
+  auto tile = [&](int x, int m) { return sb + ((m % F::ST) * F::PER + x) * F::TILE; };  // x: 0 k, 1 v, 2 q
   // a value that every lane has, as one the compiler knows to be the same in all of them
   auto same = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
   // bf16 terms of khat in the chunk from which on `left` tokens of the piece are left
@@ -486,7 +492,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       commit(one, &sh.bar_qk);
     };
     constexpr bool AHEAD = !STATES && !F::SMALL;  // q k^T of a chunk follows P v of the one before
-    auto ready = [&](int x, int m) { return __all_sync(0xFFFFFFFFu, wait_bar(&sh.full[x][m & 1], (m >> 1) & 1)); };
+    auto ready = [&](int x, int m) { return __all_sync(0xFFFFFFFFu, wait_bar(&sh.full[x][m % F::ST], (m / F::ST) & 1)); };
     if (AHEAD && end > base && ready(0, base) && ready(2, base)) qk(base);
 #pragma unroll 1
     for (int m = base; m < end; ++m, left -= C) {
@@ -504,20 +510,20 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       }
       commit(one, &sh.bar_ds);
       if (STATES) {
-        commit(one, &sh.free_[0][m & 1]);
-        commit(one, &sh.free_[1][m & 1]);
+        commit(one, &sh.free_[0][m % F::ST]);
+        commit(one, &sh.free_[1][m % F::ST]);
       } else {
         if (F::SMALL) {
           if (!ready(2, m)) break;
           qk(m);
         }
-        commit(one, &sh.free_[0][m & 1]);
+        commit(one, &sh.free_[0][m % F::ST]);
         const uint64_t qd = sdesc_sw<128>(tile(2, m));
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
           if (ks < kk) mma_ss(one, tm + F::TM_O1, qd + kstep(ks), s_desc + (uint64_t)((2048 * ks) >> 4), id_v, ks ? 1u : 0u);
         commit(one, &sh.bar_qs);
-        commit(one, &sh.free_[2][m & 1]);
+        commit(one, &sh.free_[2][m % F::ST]);
         if (!__all_sync(0xFFFFFFFFu, wait_bar(&sh.bar_p, ph))) break;
         tc_fence_after();
 #pragma unroll
@@ -560,12 +566,12 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int s = rev ? C - 1 - 32 * i - ln : 32 * i + ln;
-        sh.wk[m & 1][32 * i + ln] = s < n ? p.b * tab.pw[n - 1 - s] : 0.f;
+        sh.wk[m % F::ST][32 * i + ln] = s < n ? p.b * tab.pw[n - 1 - s] : 0.f;
       }
       __syncwarp();
     };
     auto freed = [&](int x, int m) {  // the place of tile x of chunk m
-      return m < 2 || __all_sync(0xFFFFFFFFu, wait_bar(&sh.free_[x][m & 1], ((m - 2) >> 1) & 1));
+      return m < F::ST || __all_sync(0xFFFFFFFFu, wait_bar(&sh.free_[x][m % F::ST], (m / F::ST - 1) & 1));
     };
     if constexpr (FETCH != kFetchTokens) {
       // one warp asks for a chunk's tiles in the order in which their places become free, one stores outputs, one plans
@@ -573,7 +579,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         auto fetch = [&](int x, int m, bool clean) {
           const uint32_t dst = tile(x, m);
           const CUtensorMap& map = a.map[x == 0 ? p.mk : (x == 1 ? p.mv : p.mq)];
-          uint64_t* bar = clean ? &sh.landed[x] : &sh.full[x][m & 1];
+          uint64_t* bar = clean ? &sh.landed[x] : &sh.full[x][m % F::ST];
           const int atoms = min(D / 64, ((x == 1 ? p.dv : p.dk) + 63) / 64);
           if (ln == 0) {
             mbar_arrive_expect_tx(bar, atoms * F::ATOM);
@@ -619,7 +625,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
                 for (int j = 0; j < atoms; ++j) sts128(tile(x, m) + j * F::ATOM + (r0 + i / 8) * 128 + (i % 8) * 16, 0, 0, 0, 0);
               fence_async_smem();
               __syncwarp();
-              if (ln == 0) mbar_arrive(&sh.full[x][m & 1]);
+              if (ln == 0) mbar_arrive(&sh.full[x][m % F::ST]);
             }
             ++cleaned;
           }
@@ -651,7 +657,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
               bulk_commit();
               bulk_wait_read_all();
             }
-            mbar_arrive(&sh.free_[1][m & 1]);
+            mbar_arrive(&sh.free_[1][m % F::ST]);
           }
           __syncwarp();
         }
@@ -697,7 +703,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           cp_wait<0>();
           fence_async_smem();
           __syncwarp();
-          if (ln == 0) mbar_arrive(&sh.full[x][m & 1]);
+          if (ln == 0) mbar_arrive(&sh.full[x][m % F::ST]);
         }
       }
     }
@@ -755,6 +761,15 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
 #pragma unroll
               for (int j = 0; j < 32; ++j)
                 if (cg * 32 + j < p.dv) S[j] = s0[(size_t)(cg * 32 + j) * p.dk + t];
+            }
+          } else if constexpr (STATES) {  // (no shared memory to pass them through)
+            if (key) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4)
+                if (cg * 32 + j < p.dv) {
+                  const float4 x = *reinterpret_cast<const float4*>(s0 + (size_t)t * p.dv + cg * 32 + j);
+                  S[j] = x.x, S[j + 1] = x.y, S[j + 2] = x.z, S[j + 3] = x.w;
+                }
             }
           } else {
 #pragma unroll
@@ -836,7 +851,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint64_t w = *reinterpret_cast<const uint64_t*>(&sh.wk[m & 1][s0 + 8 * (i >> 1) + 2 * (ln & 3)]);
+            const uint64_t w = *reinterpret_cast<const uint64_t*>(&sh.wk[m % F::ST][s0 + 8 * (i >> 1) + 2 * (ln & 3)]);
             x[i] = mul2(f2(__uint_as_float(r[i] << 16), __uint_as_float(r[i] & 0xFFFF0000u)), w);
           }
           const uint32_t at = tmem + (static_cast<uint32_t>(c) << 16) + s0 / 2;
@@ -980,7 +995,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
 #pragma unroll 1
       for (int m = base; m < end + (AHEAD ? 1 : 0); ++m) {
         if (m < end) {
-          wait_bar(&sh.full[0][m & 1], (m >> 1) & 1);
+          wait_bar(&sh.full[0][m % F::ST], (m / F::ST) & 1);
           if (__any_sync(0xFFFFFFFFu, timed_out || *reinterpret_cast<volatile int*>(&sh.abort))) break;
           convert_k(m, terms_of(tab, left - (AHEAD && m > base ? C : 0)), kAll);
         }
@@ -1001,7 +1016,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         for (int j = 0; j < 32; j += 4) out[(j / 4) * D] = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
       }
     } else {
-      auto full = [&](int m) { wait_bar(&sh.full[0][m & 1], (m >> 1) & 1); };
+      auto full = [&](int m) { wait_bar(&sh.full[0][m % F::ST], (m / F::ST) & 1); };
       if (!F::SMALL && left > 0) {
         full(base);
         convert_k(base, terms_of(tab, left), kAll);
@@ -1043,7 +1058,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         tc_fence_after();
         if (FETCH != kFetchTokens && n == C) put_tma(m, e);
         else put_out(m, e);
-        arrive(FETCH != kFetchTokens ? &sh.bar_out[m & 1] : &sh.free_[1][m & 1]);  // (the tile is stored from, or fetched over)
+        arrive(FETCH != kFetchTokens ? &sh.bar_out[m & 1] : &sh.free_[1][m % F::ST]);  // (the tile is stored from, or fetched over)
       }
       base += same((u.n + C - 1) / C);
       if (a.deal.handoff && !u.last) {  // to the next block
@@ -1126,8 +1141,14 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
 template <int D, bool STATES, int FETCH>
 cudaError_t run(const DecayArgs& a, cudaStream_t s) {
   using F = TcCfg<D, STATES>;
-  constexpr int smem = F::OFF_T + sizeof(TcTables);
-  const cudaError_t e = cudaFuncSetAttribute(decay_tc_kernel<D, STATES, FETCH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int smem = F::OFF_T + sizeof(TcTables<F::ST>);
+  static std::atomic<uint64_t> set{0};  // devices whose kernel has its shared memory allowed
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && !(dev < 64 && (set.load(std::memory_order_relaxed) >> dev & 1))) {
+    e = cudaFuncSetAttribute(decay_tc_kernel<D, STATES, FETCH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && dev < 64) set.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
   if (e != cudaSuccess) return e;
   return launch_pdl(decay_tc_kernel<D, STATES, FETCH>, dim3(a.deal.grid), dim3(F::NT + 128), smem, s, a);
 }
