@@ -90,7 +90,7 @@ bool size_ok(int B, int H, int L, int d_k, int d_v, bool packed) {
 bool on_tc(int dtype, int out_dtype) { return dtype == DIG_BF16 && out_dtype == DIG_BF16; }
 
 Cut cut_for(int B, int H, int L, int dk, int dv, bool packed, int nprob) {
-  return cut_of(B, H, L, dk, dv, 32, dk <= 64 && dv <= 64 ? 3 : 1, packed, nprob);
+  return cut_of(B, H, L, dk, dv, 32, dk <= 64 && dv <= 64 ? 3 : 2, packed, nprob);
 }
 
 // How the tensor-core kernel's chunks are dealt.  Uncut units need one pass; cut ones fill the GPU evenly, at the price

@@ -23,9 +23,10 @@ constexpr int C = 32;
 
 template <int D>
 struct F32Cfg {
-  static constexpr int ROW = D + 4;  // floats of a shared row: 16-byte pieces of consecutive rows on different banks
-  static constexpr int Q = 0, K = C * ROW, V = 2 * C * ROW, S = 3 * C * ROW, P = S + D * D, PW = P + C * (C + 1);
-  static constexpr int FLOATS = PW + 2 * (C + 1) + 4;
+  // Rows of q, k, v in 16-byte pieces, piece c of row t at c ^ (t & 7) (consecutive rows on different banks without
+  // padding: two blocks of D = 128 fit an SM).  P takes the place of q once q S is formed.
+  static constexpr int Q = 0, K = C * D, V = 2 * C * D, S = 3 * C * D, PW = S + D * D;
+  static constexpr int FLOATS = PW + 2 * (C + 1) + 2;
   static constexpr int SMEM = FLOATS * 4;
   static constexpr int TJ = D / 32;               // value channels per thread of an output row
   static constexpr int TC = D / 16;               // key (and value) channels of a thread's state tile
@@ -39,7 +40,7 @@ __device__ __forceinline__ float4 ld4(const T* p) {
 }
 
 template <typename T, typename TO, int D, bool STATES>
-__global__ void __launch_bounds__(256) decay_f32_kernel(const __grid_constant__ DecayArgs a) {
+__global__ void __launch_bounds__(256, D == 128 ? 2 : 3) decay_f32_kernel(const __grid_constant__ DecayArgs a) {
   using F = F32Cfg<D>;
   extern __shared__ float sm[];
   const int tid = threadIdx.x, h = blockIdx.y;
@@ -51,7 +52,8 @@ __global__ void __launch_bounds__(256) decay_f32_kernel(const __grid_constant__ 
   if (!decay_unit(a, blockIdx.x, u)) return;
   if (STATES && (u.nseg == 1 || u.i == u.nseg - 1)) return;  // a last segment's state is formed by the output pass
   const float g = a.g[h];
-  float *sq = sm + F::Q, *sk = sm + F::K, *sv = sm + F::V, *sS = sm + F::S, *sP = sm + F::P, *pw = sm + F::PW;
+  float *sq = sm + F::Q, *sk = sm + F::K, *sv = sm + F::V, *sS = sm + F::S, *sP = sq, *pw = sm + F::PW;
+  auto at = [](int t, int c) { return t * D + (((c >> 2) ^ (t & 7)) << 2); };  // piece of channel c (a multiple of four) of row t
   if (tid <= C) {
     const float2 w = decay_pow(g, tid);
     pw[tid] = w.x;
@@ -93,7 +95,7 @@ __global__ void __launch_bounds__(256) decay_f32_kernel(const __grid_constant__ 
         }
     } else {
       const float2 w = decay_pow(g, a.seg);
-#pragma unroll (TC == 4 ? 4 : 1)
+#pragma unroll 1
       for (int m = 0; m < u.i; ++m) {
         const float* ls = seg_state(seg0 + m);
 #pragma unroll
@@ -145,32 +147,27 @@ __global__ void __launch_bounds__(256) decay_f32_kernel(const __grid_constant__ 
         }
         if (c < p.dv) fv = ld4(v + row * p.vs + c);
       }
-      if (!STATES) *reinterpret_cast<float4*>(sq + t * F::ROW + c) = fq;
-      *reinterpret_cast<float4*>(sk + t * F::ROW + c) = fk;
-      *reinterpret_cast<float4*>(sv + t * F::ROW + c) = fv;
+      if (!STATES) *reinterpret_cast<float4*>(sq + at(t, c)) = fq;
+      *reinterpret_cast<float4*>(sk + at(t, c)) = fk;
+      *reinterpret_cast<float4*>(sv + at(t, c)) = fv;
     }
     __syncthreads();
     if (!STATES) {
-      {  // P: rows tid / 16 and + 16, columns tid % 16 and + 16
+      // P: rows tid / 16 and + 16, columns tid % 16 and + 16
+      float x00 = 0.f, x10 = 0.f, x11 = 0.f;  // (above the diagonal: nothing)
+      {
         const int t = tid >> 4, s = tid & 15;
-        float x00 = 0.f, x01 = 0.f, x10 = 0.f, x11 = 0.f;
 #pragma unroll 4
-        for (int c = 0; c < D; c += 4) {
-          const float4 q0 = *reinterpret_cast<const float4*>(sq + t * F::ROW + c);
-          const float4 q1 = *reinterpret_cast<const float4*>(sq + (t + 16) * F::ROW + c);
-          const float4 k0 = *reinterpret_cast<const float4*>(sk + s * F::ROW + c);
-          const float4 k1 = *reinterpret_cast<const float4*>(sk + (s + 16) * F::ROW + c);
+        for (int c = 0; c < p.dk; c += 4) {
+          const float4 q0 = *reinterpret_cast<const float4*>(sq + at(t, c));
+          const float4 q1 = *reinterpret_cast<const float4*>(sq + at(t + 16, c));
+          const float4 k0 = *reinterpret_cast<const float4*>(sk + at(s, c));
+          const float4 k1 = *reinterpret_cast<const float4*>(sk + at(s + 16, c));
           x00 += q0.x * k0.x + q0.y * k0.y + q0.z * k0.z + q0.w * k0.w;
-          x01 += q0.x * k1.x + q0.y * k1.y + q0.z * k1.z + q0.w * k1.w;
           x10 += q1.x * k0.x + q1.y * k0.y + q1.z * k0.z + q1.w * k0.w;
           x11 += q1.x * k1.x + q1.y * k1.y + q1.z * k1.z + q1.w * k1.w;
         }
-        sP[t * (C + 1) + s] = s <= t ? p.a * pw[t - s] * x00 : 0.f;
-        sP[t * (C + 1) + s + 16] = 0.f;
-        sP[(t + 16) * (C + 1) + s] = p.a * pw[t + 16 - s] * x10;
-        sP[(t + 16) * (C + 1) + s + 16] = s <= t ? p.a * pw[t - s] * x11 : 0.f;
       }
-      __syncthreads();
       constexpr int TJ = F::TJ;
       const int tb = 4 * (tid >> 5), jb = TJ * (tid & 31);
       float acc[4][TJ];
@@ -188,10 +185,10 @@ __global__ void __launch_bounds__(256) decay_f32_kernel(const __grid_constant__ 
         }
       };
 #pragma unroll 2
-      for (int c = 0; c < D; c += 4) {
+      for (int c = 0; c < p.dk; c += 4) {
         float4 qv[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(sq + (tb + i) * F::ROW + c);
+        for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(sq + at(tb + i, c));
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           float w[TJ];
@@ -210,10 +207,19 @@ __global__ void __launch_bounds__(256) decay_f32_kernel(const __grid_constant__ 
 #pragma unroll
         for (int j = 0; j < TJ; ++j) acc[i][j] *= w;
       }
+      __syncthreads();  // q is no longer read
+      {
+        const int t = tid >> 4, s = tid & 15;
+        sP[t * (C + 1) + s] = s <= t ? p.a * pw[t - s] * x00 : 0.f;
+        sP[t * (C + 1) + s + 16] = 0.f;
+        sP[(t + 16) * (C + 1) + s] = p.a * pw[t + 16 - s] * x10;
+        sP[(t + 16) * (C + 1) + s + 16] = s <= t ? p.a * pw[t - s] * x11 : 0.f;
+      }
+      __syncthreads();
 #pragma unroll 4
-      for (int s = 0; s < C; ++s) {
+      for (int s = 0; s < min(C, tb + 4); ++s) {  // the warp's last row
         float w[TJ];
-        ldj(sv + s * F::ROW + jb, w);
+        ldj(sv + at(s, jb & ~3) + (jb & 3), w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float x = sP[(tb + i) * (C + 1) + s];
@@ -231,21 +237,22 @@ __global__ void __launch_bounds__(256) decay_f32_kernel(const __grid_constant__ 
         }
       }
     }
-    // ---- the state after the chunk
+    // ---- the state after the chunk, if anything needs it
+    if (!STATES && t0 + C >= u.n && !(p.Sf && u.slot >= 0 && u.i == u.nseg - 1)) break;
     const float wh = pw[n - e], wl = pw[C + 1 + n - e];
 #pragma unroll
     for (int i = 0; i < TC; ++i)
 #pragma unroll
       for (int j = 0; j < TC; ++j) S[i][j] = fmaf(wh, S[i][j], wl * S[i][j]);
 #pragma unroll 2
-    for (int s = 0; s < n; ++s) {
+    for (int s = 0; s < (c0 < p.dk ? n : 0); ++s) {
       const float w = p.b * pw[n - 1 - s];
       float kc[TC], vc[TC];
 #pragma unroll
       for (int i = 0; i < TC; i += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(sk + s * F::ROW + c0 + i);
+        const float4 x = *reinterpret_cast<const float4*>(sk + at(s, c0 + i));
         kc[i] = w * x.x, kc[i + 1] = w * x.y, kc[i + 2] = w * x.z, kc[i + 3] = w * x.w;
-        const float4 y = *reinterpret_cast<const float4*>(sv + s * F::ROW + jcol(i));
+        const float4 y = *reinterpret_cast<const float4*>(sv + at(s, jcol(i)));
         vc[i] = y.x, vc[i + 1] = y.y, vc[i + 2] = y.z, vc[i + 3] = y.w;
       }
 #pragma unroll

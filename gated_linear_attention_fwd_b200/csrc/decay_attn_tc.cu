@@ -444,10 +444,11 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   auto tile = [&](int x, int m) { return sb + ((m % F::ST) * F::PER + x) * F::TILE; };  // x: 0 k, 1 v, 2 q
   // a value that every lane has, as one the compiler knows to be the same in all of them
   auto same = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
-  // bf16 terms of khat in the chunk from which on `left` tokens of the piece are left
+  // bf16 terms of khat in the chunk from which on `left` tokens of the piece are left (0: nothing needs the state after it)
   auto terms_of = [&](const TcPiece& t, int left) {
     const int after = t.u.len - t.u.t0 - t.u.n + left - C;  // tokens of the sequence after the chunk
-    return same(t.keep && t.g * max(after, 0) >= -7.f ? 3 : 2);
+    const bool needed = STATES || left > C || (t.u.last ? t.keep : a.deal.handoff);
+    return same(!needed ? 0 : t.keep && t.g * max(after, 0) >= -7.f ? 3 : 2);
   };
   // Waits, as long as wait_bar would, for another block's flag.
   auto wait_flag = [&](const uint32_t* f) {
@@ -834,6 +835,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     // formed again once its place is free (held in registers meanwhile it would push others out to local memory).
     auto convert_k = [&](int m, int terms, auto last) {
       constexpr bool LAST = decltype(last)::value;
+      if (terms == 0) return;
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         const int c = 32 * (warp & 3) + 16 * half;
@@ -1041,7 +1043,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         }
         wait_bar(&sh.bar_ds, ph);
         tc_fence_after();
-        update(n, e);  // before P v, which comes to stand in dS's place
+        if (terms) update(n, e);  // before P v, which comes to stand in dS's place
         if (F::SMALL) {
           wait_bar(&sh.bar_qk, ph);
           tc_fence_after();
