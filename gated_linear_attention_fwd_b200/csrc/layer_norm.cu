@@ -137,11 +137,11 @@ struct LnArgs {
   int D;
 };
 
-// Rows in registers: NV vectors of V values per thread, TPR threads per row.  Left to itself the compiler takes some 80
-// registers, faster than 64 with their spills (33554 x 1000 bf16: 27 against 39 us); only with 512 threads a
-// block, of which an SM would hold one, the second block wins (4096 x 8192 bf16: 30 against 38 us).
+// Rows in registers: NV vectors of V values per thread, TPR threads per row.  Blocks an SM: three of 256 threads (80
+// registers; 64 with their spills took 39 us for 33554 x 1000 bf16 values where 80 took 27, and a hundred took 55 for
+// 16384 x 4096 where 80 took 48); of 512 threads two, where one took 38 us for 4096 x 8192 bf16 values and two 30.
 template <typename T, typename TO, int V, int NV, int TPR>
-__global__ void __launch_bounds__(threads_of<TPR>, TPR == 512 && V == 8 ? 2 : 1) ln_fwd_kernel(const LnArgs a) {
+__global__ void __launch_bounds__(threads_of<TPR>, (V == 1 ? (TPR == 512 ? 1 : 2) : TPR == 512 ? (V == 8 ? 2 : 1) : 3)) ln_fwd_kernel(const LnArgs a) {
   constexpr int NT = threads_of<TPR>, RPB = NT / TPR;
   __shared__ float red[2 * NT / 32];
   const int tr = threadIdx.x % TPR;
