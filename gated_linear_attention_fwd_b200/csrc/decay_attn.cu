@@ -82,7 +82,7 @@ bool al4(const void* p, int dtype) { return (reinterpret_cast<uintptr_t>(p) & (d
 // Sizes a kernel can address: rows and segment slots in int, elements in 2^40.
 bool size_ok(int B, int H, int L, int d_k, int d_v, bool packed) {
   const long long rows = packed ? L : (long long)B * L;
-  return rows <= 2147483647ll && rows * H * (d_k > d_v ? d_k : d_v) < (1ll << 40) && (long long)B + L <= 2147483647ll &&
+  return rows <= 2147483647ll - 256 && rows * H * (d_k > d_v ? d_k : d_v) < (1ll << 40) && (long long)B + L <= 2147483647ll &&
          H <= 65535;
 }
 
@@ -93,10 +93,12 @@ Cut cut_for(int B, int H, int L, int dk, int dv, bool packed, int nprob) {
   return cut_of(B, H, L, dk, dv, 32, dk <= 64 && dv <= 64 ? 3 : 2, packed, nprob);
 }
 
-// How the tensor-core kernel's chunks are dealt.  Uncut units need one pass; cut ones fill the GPU evenly, at the price
-// of a first pass over the cut parts' k and v (0.42 of the second's time a chunk: it reads half as much), its launch,
-// and joining the earlier blocks' states (a tenth of a chunk's time each, at 128 x 128).  Packed sequences, whose
-// lengths the host does not know, are taken to be alike.
+// How the tensor-core kernel's chunks are dealt.  Uncut units need one pass.  Cut ones fill the GPU evenly; where a block's
+// run is a whole unit at least, the state passes from block to block, still in one pass (backward of 4 x 4096 tokens, 16
+// heads of 128/128, 192 units on 148 blocks: 215 us, uncut 257, in two passes 281).  Else a first pass forms the cut
+// parts' states, at 0.42 of the second's time a chunk (it reads half as much), with its launch and the joining of the
+// earlier blocks' states (a tenth of a chunk's time each).  Packed sequences, whose lengths the host does not know, are
+// taken to be alike.
 struct Deal {
   DecayDeal d;
   int D;
@@ -131,10 +133,11 @@ Deal deal_for(int B, int H, int L, int dk, int dv, bool packed, int nprob) {
     r.d.handoff = 1;
   }
   r.multi = cuttable && r.d.gran == 1 && !r.d.handoff;
-  // Six and more blocks to a unit: joining each block's predecessors in the second pass costs some half a microsecond
-  // apiece, a kernel that joins them all once three (2 x 12544 tokens, 6 heads of 32/64: KJOIN).
-  r.d.second = r.multi;
-  r.d.joined = r.multi && !packed && (long long)n * r.d.grid >= 6 * total;
+  // Joining its predecessors' states costs a block of the second pass time for each of them; a kernel that joins them all
+  // costs a launch, and the second pass cannot start early.  fwd, bf16, without and with that kernel: 2 x 12544 tokens, 6
+  // heads of 32/64, 25 blocks to a unit, 54 and 58 us; 4096, one of 64/64, 32 blocks, 25.4 and 24.5; 8192, 4 of 64/64,
+  // 64 blocks, 31.0 and 27.7; 16384, 2 of 128/128, 64 blocks, 50 and 37.
+  r.d.joined = r.multi && !packed && (long long)n * r.d.grid >= 32 * total;
   r.states = r.d.handoff ? (size_t)r.d.grid * r.D * r.D : r.multi ? (size_t)2 * r.d.grid * r.D * r.D : 0;
   return r;
 }

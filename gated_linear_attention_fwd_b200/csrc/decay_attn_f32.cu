@@ -1,6 +1,6 @@
 // decay_attn_f32.cu -- head-decay linear attention on the FP32 pipes: the kernel
 // of fp32 inputs, whose products the tensor core would have to take as six pairs
-// of bf16 terms each.
+// of bf16 terms each, and of fp32 outputs.
 //
 // One block of 256 threads walks a segment in chunks of 32 tokens.  With the
 // chunk's q, k, v rows and the state S in shared memory:
@@ -10,6 +10,11 @@
 // S also stays in registers (a tile per thread), so that it is read from shared
 // memory only as the operand of q S.  lambda^n is applied as hi + lo: a rounded
 // power, applied once a chunk, would drift over a long sequence.
+//
+// Shared-memory reads bound the products of 32 tokens (q S, P v: 5 reads of 16 bytes
+// for 16 multiply-adds of a thread), a block's chain the small calls: 4 x 1024 tokens,
+// 16 heads of 128/128, 296 us, 14.5 TFLOP/s of the recurrent form's operations (one
+// block an SM, with padded rows: 347 us); 8 x 256 tokens, 6 heads of 64/64, 22 us.
 #include <cuda_bf16.h>
 
 #include "decay_attn.h"
