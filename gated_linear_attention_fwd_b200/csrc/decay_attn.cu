@@ -117,28 +117,22 @@ Deal deal_for(int B, int H, int L, int dk, int dv, bool packed, int nprob) {
   double best = packed && cuttable ? 1e30 : (double)((units + r.d.grid - 1) / r.d.grid) * n;  // packed: dealt by the chunk
   if (cuttable) {
     for (long long c = (total + slots - 1) / slots, k = 0; k < 64 && (k == 0 || c <= n); ++c, ++k) {
-      const double cost = c + 0.42 * (c < n ? c : n - 1) + 2.0 + 0.1 * ((n + c - 1) / c);
+      const int grid = (int)((total + c - 1) / c);
+      const double per_unit = (double)n * grid / total;  // blocks
+      const bool two = !packed && per_unit >= 32;
+      const double cost = c + (two ? 0.42 * c + 3.0 : (per_unit <= 1.0 ? 0.5 : 0.5 * c + 0.1 * per_unit));
       if (cost < best) {
         best = cost;
-        r.d.grid = (int)((total + c - 1) / c);
+        r.d.grid = grid;
         r.d.gran = 1;
+        r.d.handoff = !two;
       }
     }
   }
   if (packed) r.d.gran = 1;
-  // units no longer than a run, so that each is cut once at most: one pass, the state handed from block to block
-  if (!packed && cuttable && deal_div(total, slots) >= n && (double)((total + slots - 1) / slots) + 1.0 < best) {
-    r.d.grid = (int)slots;
-    r.d.gran = 1;
-    r.d.handoff = 1;
-  }
   r.multi = cuttable && r.d.gran == 1 && !r.d.handoff;
-  // Joining its predecessors' states costs a block of the second pass time for each of them; a kernel that joins them all
-  // costs a launch, and the second pass cannot start early.  fwd, bf16, without and with that kernel: 2 x 12544 tokens, 6
-  // heads of 32/64, 25 blocks to a unit, 54 and 58 us; 4096, one of 64/64, 32 blocks, 25.4 and 24.5; 8192, 4 of 64/64,
-  // 64 blocks, 31.0 and 27.7; 16384, 2 of 128/128, 64 blocks, 50 and 37.
-  r.d.joined = r.multi && !packed && (long long)n * r.d.grid >= 32 * total;
-  r.states = r.d.handoff ? (size_t)r.d.grid * r.D * r.D : r.multi ? (size_t)2 * r.d.grid * r.D * r.D : 0;
+  r.d.second = r.d.joined = r.multi;
+  r.states = r.d.handoff || r.multi ? (size_t)2 * r.d.grid * r.D * r.D : 0;
   return r;
 }
 

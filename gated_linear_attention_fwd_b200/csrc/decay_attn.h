@@ -46,9 +46,10 @@ struct DecayDeal {
   int chunks;   // of a unit (without cu)
   int nprob;
   int second;   // whether a first pass of the same call runs before
-  // Whether a block hands the state at its run's end to the next one (units no longer than a run): it walks the beginning
-  // of its last unit first and the end of its first unit last, so that the state is there long before it is asked for.
-  // Blocks are numbered as they start, and wait only for lower numbers.
+  // Whether one pass does it, the blocks handing states on: a block first makes known what its last unit's part in the run
+  // adds to the state (walking that part for its state alone, unless it may be walked in full at once), and comes to the
+  // end of its first unit, which needs the states of the blocks before it, last.  Blocks are numbered as they start, and
+  // wait only for lower numbers, which wait for nothing before they hand on.
   int handoff;
   int joined;   // whether the blocks' states are joined by a kernel of their own
 };
@@ -177,6 +178,7 @@ struct DecayPiece {
   int first, len;        // the sequence's first row and length
   int t0, n;             // the piece's first scan position and its tokens
   int chunks;            // of the piece
+  int unit_chunks;       // of the unit
   bool last;             // whether the unit ends with it
   int slot;              // state of the sequence, -1: none
   long long unit_start;  // the unit's first chunk among all units'
@@ -241,6 +243,7 @@ __device__ __forceinline__ void decay_piece(const DecayArgs& a, long long per, l
     }
   }
   u.chunks = (int)min((long long)(nch - c0), r1 - r);
+  u.unit_chunks = nch;
   u.last = c0 + u.chunks == nch;
   u.t0 = 128 * c0;
   u.n = max(min(u.len - u.t0, 128 * u.chunks), 0);

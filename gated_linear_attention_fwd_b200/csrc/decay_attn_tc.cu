@@ -268,6 +268,8 @@ struct TcPiece {
   int j0;                     // the first block whose state is to be joined
   int rem;                    // the blocks before this one have the longer runs
   long long run;              // chunks of the shorter runs
+  int state;                  // only the state is formed
+  int publish;                // the state at its end is handed on
   int more;                   // 0: there is no such piece
 };
 
@@ -282,7 +284,12 @@ struct TcTables {
   uint64_t bar_qk, bar_ds, bar_qs, bar_pv, bar_end;  // the tensor core's
   uint64_t bar_out[2];              // the outputs of chunk m are staged, m & 1
   // how the chunks are dealt, and what of this block's run is left
-  long long per, at, end, first, first_end;
+  long long per, at, end;
+  struct {
+    long long at, end;
+    int state, publish;
+  } todo[4];                        // what of the run comes after that, in order
+  int next;
   int me;                           // this block's number
   uint32_t tmem;
   int abort;
@@ -362,33 +369,58 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     const long long grains = deal_div(per * a.H * a.deal.nprob, a.deal.gran);
     const int grid = (int)min((long long)a.deal.grid, grains);
     const DealRuns runs(grains, grid);
-    long long r, r1, first, first_end;  // the next piece's start, the last's end; a piece left for last
-    int me = blockIdx.x;
+    long long r = 0, r1 = 0;  // what comes next
+    int me = blockIdx.x, state = 0, publish = 0;
     if (k == 0) {
       if (a.deal.handoff) {
         if (ln == 0) me = (int)atomicAdd(a.counter, 1u);
         me = __shfl_sync(0xFFFFFFFFu, me, 0);
       }
-      r = on && me < grid ? runs.start(me) * a.deal.gran : 0;
-      r1 = on && me < grid ? runs.start(me + 1) * a.deal.gran : 0;
-      first = first_end = 0;
-      if (a.deal.handoff && r < r1) {  // the end of the run's first unit comes last
-        const long long n = a.deal.chunks;
-        first = r;
-        first_end = r = deal_div(r + n - 1, n) * n;
+      if (on && me < grid) {
+        r = runs.start(me) * a.deal.gran;
+        r1 = runs.start(me + 1) * a.deal.gran;
+      }
+      if (ln == 0) sh.next = 4;
+      if (a.deal.handoff && r < r1) {
+        DecayPiece u;
+        decay_piece(a, per, r, r1, u);  // the run's first unit: what is left of it, unless the run starts with it
+        const long long head = u.unit_start < r ? min(u.unit_start + u.unit_chunks, r1) : r;
+        decay_piece(a, per, r1 - 1, r1, u);  // and its last: what the run has of it, unless it ends there
+        const bool open = !u.last;
+        const long long tail = open ? max(r, u.unit_start) : r1;
+        // walked in full at once where it begins with the unit and the next block can end that
+        const bool once = u.unit_start >= r && u.unit_start + u.unit_chunks <= runs.start(min(me + 2, grid));
+        if (ln == 0) {
+          int i = 4;
+          auto put = [&](long long at, long long end, int st, int pub) {
+            if (at < end) {
+              --i;
+              sh.todo[i].at = at, sh.todo[i].end = end, sh.todo[i].state = st, sh.todo[i].publish = pub;
+            }
+          };
+          const bool middle = open && u.unit_start < r;  // the run is a part of one unit
+          if (!middle) put(r, head, 0, 0);
+          if (open && !once) put(tail, r1, 0, 0);
+          if (!middle) put(head, tail, 0, 0);
+          if (open) put(tail, r1, !once, 1);
+          sh.next = i;
+        }
+        r = r1 = 0;
       }
     } else {
       me = sh.me;
       r = sh.at;
       r1 = sh.end;
-      first = sh.first;
-      first_end = sh.first_end;
     }
-    // the beginning of the run's last unit comes first: [r1 - tail, r1)
-    const bool tail_first = k == 0 && a.deal.handoff && r1 % a.deal.chunks != 0;
-    const long long next = r, next_end = tail_first ? deal_div(r1, a.deal.chunks) * a.deal.chunks : r1;
-    if (tail_first) r = next_end;
-    else if (a.deal.handoff && r >= r1) r = first, r1 = first_end, first = first_end;
+    __syncwarp();
+    int next = sh.next;
+    if (r >= r1 && next < 4) {
+      r = sh.todo[next].at;
+      r1 = sh.todo[next].end;
+      state = sh.todo[next].state;
+      publish = sh.todo[next].publish;
+      ++next;
+    }
     __syncwarp();
     bool more = r < r1;
     if (more) {
@@ -403,24 +435,25 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         t.u = u;
         t.g = a.g[u.h];
         t.keep = a.p[u.z].Sf && u.slot >= 0;
-        t.j0 = a.deal.joined || a.deal.handoff ? me - 1 : runs.block_of(u.unit_start);
+        t.j0 = a.deal.joined ? me - 1 : runs.block_of(u.unit_start);
+        t.state = state;
+        t.publish = publish;
         t.rem = runs.rem;
         t.run = runs.q;
       }
-      if (k > 0 && more && u.t0 == 0 && u.last && a.p[u.z].S0 && u.slot >= 0) {  // on the way to L2 by the time the piece starts
+      if (k > 0 && more && u.t0 == 0 && (u.last || publish) && a.p[u.z].S0 && u.slot >= 0) {  // on the way to L2 by the time the piece starts
         const DecayProblem& p = a.p[u.z];
         const char* s0 = reinterpret_cast<const char*>(p.S0 + ((size_t)u.slot * a.H + u.h) * p.dk * p.dv);
         for (int i = 128 * ln; i < 4 * p.dk * p.dv; i += 128 * 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(s0 + i));
       }
-      r = STATES ? r1 : tail_first ? next : r + u.chunks;
+      r = STATES ? r1 : r + u.chunks;
     }
     if (ln == 0) {
       t.more = more;
       sh.per = per;
       sh.at = r;
-      sh.end = tail_first ? next_end : r1;
-      sh.first = first;
-      sh.first_end = first_end;
+      sh.end = r1;
+      sh.next = next;
       sh.me = me;
     }
     __syncwarp();
@@ -462,7 +495,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   // bf16 terms of khat in the chunk from which on `left` tokens of the piece are left (0: nothing needs the state after it)
   auto terms_of = [&](const TcPiece& t, int left) {
     const int after = t.u.len - t.u.t0 - t.u.n + left - C;  // tokens of the sequence after the chunk
-    const bool needed = STATES || left > C || (t.u.last ? t.keep : a.deal.handoff);
+    const bool needed = STATES || left > C || t.publish || (t.u.last && t.keep);
     return same(!needed ? 0 : t.keep && t.g * max(after, 0) >= -7.f ? 3 : 2);
   };
   // Waits, as long as wait_bar would, for another block's flag.
@@ -509,7 +542,11 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     };
     constexpr bool AHEAD = !STATES && !F::SMALL;  // q k^T of a chunk follows P v of the one before
     auto ready = [&](int x, int m) { return __all_sync(0xFFFFFFFFu, wait_bar(&sh.full[x][m % F::ST], (m / F::ST) & 1)); };
-    if (AHEAD && end > base && ready(0, base) && ready(2, base)) qk(base);
+    const bool state = !STATES && same(tab.state);
+    if (AHEAD && end > base && ready(0, base) && ready(2, base)) {
+      if (state) commit(one, &sh.bar_qk);
+      else qk(base);
+    }
 #pragma unroll 1
     for (int m = base; m < end; ++m, left -= C) {
       const uint32_t ph = m & 1;
@@ -531,17 +568,19 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       } else {
         if (F::SMALL) {
           if (!ready(2, m)) break;
-          qk(m);
+          if (state) commit(one, &sh.bar_qk);
+          else qk(m);
         }
         commit(one, &sh.free_[0][m % F::ST]);
         const uint64_t qd = sdesc_sw<128>(tile(2, m));
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
-          if (ks < kk) mma_ss(one, tm + F::TM_O1, qd + kstep(ks), s_desc + (uint64_t)((2048 * ks) >> 4), id_v, ks ? 1u : 0u);
+          if (ks < kk && !state) mma_ss(one, tm + F::TM_O1, qd + kstep(ks), s_desc + (uint64_t)((2048 * ks) >> 4), id_v, ks ? 1u : 0u);
         commit(one, &sh.bar_qs);
         commit(one, &sh.free_[2][m % F::ST]);
         if (!__all_sync(0xFFFFFFFFu, wait_bar(&sh.bar_p, ph))) break;
         tc_fence_after();
+        if (!state)
 #pragma unroll
         for (int i = 1; i >= 0; --i)  // a K-step's 16 columns: 8 of the first term, 8 of the second
 #pragma unroll
@@ -550,7 +589,8 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         commit(one, &sh.bar_pv);
         if (AHEAD && m + 1 < end) {
           if (!ready(0, m + 1) || !ready(2, m + 1)) break;
-          qk(m + 1);
+          if (state) commit(one, &sh.bar_qk);
+          else qk(m + 1);
         }
       }
     }
@@ -627,7 +667,8 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           fetch(0, m, clean);
           if (!STATES) {
             if (!freed(2, m)) break;
-            fetch(2, m, false);
+            if (!tab.state) fetch(2, m, false);
+            else if (ln == 0) mbar_arrive(&sh.full[2][m % F::ST]);  // nothing reads q
           }
           if (!freed(1, m)) break;
           fetch(1, m, clean);
@@ -656,7 +697,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           if (!__all_sync(0xFFFFFFFFu, wait_bar(&sh.bar_out[m & 1], (m >> 1) & 1))) break;
           const int t0 = u.t0 + (m - base) * C;
           if (ln == 0) {
-            if (u.n - (m - base) * C >= C) {
+            if (u.n - (m - base) * C >= C && !tab.state) {
               const uint32_t src = tile(1, m);
               if constexpr (FETCH == kFetchRows) {
                 const int r = (rev ? u.len - t0 - C : t0) + (a.cu ? u.first : 0);
@@ -690,6 +731,10 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
 #pragma unroll 1
         for (int m = base; m < end; ++m) {
           if (!freed(x, m)) break;
+          if (x == 2 && !STATES && tab.state) {  // nothing reads q
+            if (ln == 0) mbar_arrive(&sh.full[2][m % F::ST]);
+            continue;
+          }
           const uint32_t dst = tile(x, m);
           if (x == 0) weights(m, min(C, u.n - (m - base) * C));
           int row[4];  // of tokens ln, ln + 32, ..
@@ -752,8 +797,9 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     const int nv = (p.dv + 15) / 16 * 16;           // columns of the products with v or S
     const bool key = t < D && t < p.dk;             // this lane holds a key channel of the state
     // ---- the state the piece starts from: lane t = key channel, value channels 32 cg ..
-    if (!STATES && a.deal.handoff && u.t0 > 0) {  // the state of the block before
-      if (ln == 0) wait_flag(a.flag + sh.me - 1);
+    const bool state = !STATES && same(tab.state);
+    if (!STATES && a.deal.handoff && u.t0 > 0 && !state) {  // the states of the blocks before
+      for (int i = tab.j0 + ln; i < sh.me; i += 32) wait_flag(a.flag + i);
       __syncwarp();
     }
     float S[32];
@@ -769,7 +815,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     // element (c, j) of a block's state: four value channels of consecutive key channels side by side
     auto block_state = [&](int i) { return reinterpret_cast<float4*>(a.segst + (size_t)i * (D * D)) + (cg * 8) * D + t; };
     if (t < D) {
-      if (u.t0 == 0 && (STATES || u.last || a.deal.handoff)) {
+      if (u.t0 == 0 && (STATES || u.last || tab.publish)) {
         if (p.S0 && u.slot >= 0) {
           const float* s0 = p.S0 + ((size_t)u.slot * a.H + h) * p.dk * p.dv;
           if (p.s0_t) {
@@ -807,14 +853,14 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
             }
           }
         }
-        if (STATES) {  // a copy for the second pass, in which the unit's last block may already have written S_final there
-          float4* s0 = block_state(a.deal.grid + blockIdx.x);
+        if (STATES || state) {  // a copy for the walk in full, when the unit's last block may already have written S_final there
+          float4* s0 = block_state(a.deal.grid + sh.me);
 #pragma unroll
           for (int j = 0; j < 32; j += 4) s0[(j / 4) * D] = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
         }
-      } else if (!STATES) {
+      } else if (!STATES && !state) {
         // the states of the blocks that have walked the unit so far; at its start, the copy of S0
-        const int j0 = u.t0 > 0 ? tab.j0 : a.deal.grid + blockIdx.x, j1 = u.t0 > 0 ? sh.me : j0 + 1;
+        const int j0 = u.t0 > 0 ? tab.j0 : a.deal.grid + sh.me, j1 = u.t0 > 0 ? sh.me : j0 + 1;
 #pragma unroll 2
         for (int i = j0; i < j1; ++i) {
           const float4* ls = block_state(i);
@@ -844,7 +890,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     };
     if constexpr (!STATES) {
       named_bar(9, NT);  // S0 came through the same memory
-      if (left > 0) put_state();
+      if (left > 0 && !state) put_state();
     }
     // khat^T of chunk m -> tensor memory: the warp's 32 channels, its group's tokens.  LAST: the last of three terms alone,
     // formed again once its place is free (held in registers meanwhile it would push others out to local memory).
@@ -1051,7 +1097,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         if (F::SMALL) convert_k(m, terms, kAll);
         else if (terms == 3) convert_k(m, terms, kThird);
         arrive(&sh.bar_k);
-        if (!F::SMALL) {
+        if (!F::SMALL && !state) {
           wait_bar(&sh.bar_qk, ph);
           tc_fence_after();
           convert_p();
@@ -1059,26 +1105,28 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         wait_bar(&sh.bar_ds, ph);
         tc_fence_after();
         if (terms) update(n, e);  // before P v, which comes to stand in dS's place
-        if (F::SMALL) {
+        if (F::SMALL && !state) {
           wait_bar(&sh.bar_qk, ph);
           tc_fence_after();
           convert_p();
         }
         arrive(&sh.bar_p);
-        wait_bar(&sh.bar_qs, ph);
-        if (left > C) put_state();  // (S_final leaves through the same memory)
+        if (!state) wait_bar(&sh.bar_qs, ph);
+        if (left > C && !state) put_state();  // (S_final leaves through the same memory)
         if (!F::SMALL && left > C) {  // while the tensor core is at P v
           full(m + 1);
           convert_k(m + 1, terms_of(tab, left - C), kAll);
         }
-        wait_bar(&sh.bar_pv, ph);
-        tc_fence_after();
-        if (FETCH != kFetchTokens && n == C) put_tma(m, e);
-        else put_out(m, e);
+        if (!state) {
+          wait_bar(&sh.bar_pv, ph);
+          tc_fence_after();
+          if (FETCH != kFetchTokens && n == C) put_tma(m, e);
+          else put_out(m, e);
+        }
         arrive(FETCH != kFetchTokens ? &sh.bar_out[m & 1] : &sh.free_[1][m % F::ST]);  // (the tile is stored from, or fetched over)
       }
       base += same((u.n + C - 1) / C);
-      if (a.deal.handoff && !u.last) {  // to the next block
+      if (tab.publish) {  // to the blocks that go on
         if (t < D) {
           float4* out = block_state(sh.me);
 #pragma unroll
@@ -1088,7 +1136,6 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         named_bar(9, NT);
         if (tid == 0) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(a.flag + sh.me), "r"(1u) : "memory");
       }
-      if (a.deal.handoff && u.t0 > 0 && tid == 0) a.flag[sh.me - 1] = 0u;  // every warp has seen it: all are past this unit's chunks
       if (tab.keep && u.last && 32 * (warp & 3) < D) {
         // dS0 = lambda G_0; an empty sequence passes its state on as it is
         const float w = p.lag && u.len > 0 ? tab.pw[1] : 1.f;
@@ -1119,7 +1166,14 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   __syncthreads();
   tc_fence_after();
   if (warp == W0) tmem_dealloc(tmem, F::TM_COLS);
-  if (a.deal.handoff && tid == 0 && atomicAdd(a.counter + 1, 1u) == gridDim.x - 1) a.counter[0] = a.counter[1] = 0u;
+  if (a.deal.handoff) {  // the last block to end leaves counters and flags as they were
+    if (tid == 0) sh.abort = atomicAdd(a.counter + 1, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (sh.abort) {
+      for (int i = tid; i < a.deal.grid; i += NT + 128) a.flag[i] = 0u;
+      if (tid < 2) a.counter[tid] = 0u;
+    }
+  }
 }
 
 // The states that the first pass left, joined in place: block i's then is its unit's state up to the end of its run.
