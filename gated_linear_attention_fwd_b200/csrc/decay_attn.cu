@@ -93,12 +93,17 @@ Cut cut_for(int B, int H, int L, int dk, int dv, bool packed, int nprob) {
   return cut_of(B, H, L, dk, dv, 32, dk <= 64 && dv <= 64 ? 3 : 2, packed, nprob);
 }
 
-// How the tensor-core kernel's chunks are dealt.  Uncut units need one pass.  Cut ones fill the GPU evenly; where a block's
-// run is a whole unit at least, the state passes from block to block, still in one pass (backward of 4 x 4096 tokens, 16
-// heads of 128/128, 192 units on 148 blocks: 215 us, uncut 257, in two passes 281).  Else a first pass forms the cut
-// parts' states, at 0.42 of the second's time a chunk (it reads half as much), with its launch and the joining of the
-// earlier blocks' states (a tenth of a chunk's time each).  Packed sequences, whose lengths the host does not know, are
-// taken to be alike.
+// How the tensor-core kernel's chunks are dealt.  Costs in chunks of a block's time:
+//   - uncut units: the most that one block gets of them;
+//   - cut, one pass (the blocks hand states on): the run, and half of it again where a unit spans more than two blocks
+//     (their parts are walked for the state first), some 2.5 for starts and waits, a tenth for each state joined.
+//     Backward of 4 x 4096 tokens, 16 heads of 128/128, 192 units on 148 blocks: 215 us, uncut 257, in two passes 281;
+//     7 packed prompts of 16382 tokens, 16 heads of 128/128: 115 us, in two passes 124; 2 x 12544 tokens, 6 heads of
+//     32/64, 25 blocks to a unit: 54 us, in two passes 60;
+//   - cut, two passes with a kernel between that joins the states, where a unit has 32 blocks and more: joining would cost
+//     each block more than the two launches do (16384 tokens, 2 heads of 128/128, 64 blocks: 37 us, joined by the blocks
+//     of the second pass 50; 8192, 4 of 64/64: 28 and 31; 4096, one of 64/64, 32 blocks: 24.5 and 25.4).
+// Packed sequences, whose lengths the host does not know, are taken to be alike and always dealt by the chunk.
 struct Deal {
   DecayDeal d;
   int D;
@@ -112,15 +117,18 @@ Deal deal_for(int B, int H, int L, int dk, int dv, bool packed, int nprob) {
   const long long units = (long long)B * H * nprob;
   const int n = packed ? (int)(((long long)L / 128 + B) / (B > 0 ? B : 1)) : (L > 128 ? (L + 127) / 128 : 1);
   const long long total = units * (n > 0 ? n : 1);
-  r.d = DecayDeal{(int)(units < slots ? units : slots), n, n, nprob, 0, 0, 0};
+  r.d = DecayDeal{(int)(units < slots ? units : slots), n, n, nprob, 0, 0};
   const bool cuttable = packed ? L > 128 : n > 1;
-  double best = packed && cuttable ? 1e30 : (double)((units + r.d.grid - 1) / r.d.grid) * n;  // packed: dealt by the chunk
-  if (cuttable) {
+  double best = (double)((units + r.d.grid - 1) / r.d.grid) * n;
+  if (cuttable && packed) {
+    r.d.grid = (int)(total < slots ? total : slots);
+    r.d.handoff = 1;
+  } else if (cuttable) {
     for (long long c = (total + slots - 1) / slots, k = 0; k < 64 && (k == 0 || c <= n); ++c, ++k) {
-      const int grid = (int)((total + c - 1) / c);
+      const int grid = (int)(k == 0 && total >= slots ? slots : (total + c - 1) / c);
       const double per_unit = (double)n * grid / total;  // blocks
-      const bool two = !packed && per_unit >= 32;
-      const double cost = c + (two ? 0.42 * c + 3.0 : (per_unit <= 1.0 ? 0.5 : 0.5 * c + 0.1 * per_unit));
+      const bool two = per_unit >= 32;
+      const double cost = c + (two ? 0.42 * c + 3.0 : (per_unit <= 1.0 ? 1.0 : 0.45 * c + 2.5 + 0.1 * per_unit));
       if (cost < best) {
         best = cost;
         r.d.grid = grid;
@@ -131,7 +139,7 @@ Deal deal_for(int B, int H, int L, int dk, int dv, bool packed, int nprob) {
   }
   if (packed) r.d.gran = 1;
   r.multi = cuttable && r.d.gran == 1 && !r.d.handoff;
-  r.d.second = r.d.joined = r.multi;
+  r.d.joined = r.multi;
   r.states = r.d.handoff || r.multi ? (size_t)2 * r.d.grid * r.D * r.D : 0;
   return r;
 }

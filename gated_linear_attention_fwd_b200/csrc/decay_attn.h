@@ -45,13 +45,12 @@ struct DecayDeal {
   int gran;
   int chunks;   // of a unit (without cu)
   int nprob;
-  int second;   // whether a first pass of the same call runs before
   // Whether one pass does it, the blocks handing states on: a block first makes known what its last unit's part in the run
   // adds to the state (walking that part for its state alone, unless it may be walked in full at once), and comes to the
   // end of its first unit, which needs the states of the blocks before it, last.  Blocks are numbered as they start, and
   // wait only for lower numbers, which wait for nothing before they hand on.
   int handoff;
-  int joined;   // whether the blocks' states are joined by a kernel of their own
+  int joined;   // else: a first pass forms the states of the cut parts, and a kernel of their own joins them
 };
 
 // How the tensor-core kernel fetches tiles: token by token, or by TMA from whole-row or column maps.
@@ -73,7 +72,7 @@ struct DecayArgs {
   DecayDeal deal;
   uint32_t* flag;     // [block] a block's state has been handed over (left zero)
   uint32_t* counter;  // blocks started, blocks done (left zero)
-  float* segst;   // tensor core: [2][block][D * D], a block's unfinished unit's state and the copy of its S0; else [problem][segment][H][D * D] segment states
+  float* segst;   // tensor core: [2][block][D * D], what a block's cut unit adds to its state, and the copy of its S0; else [problem][segment][H][D * D] segment states
   long long segst_problem;  // elements between problems there
   uint32_t* status;
 };

@@ -38,18 +38,18 @@
 //
 // The chunks of all sequences, heads and (backward) problems are dealt to the blocks
 // in equal runs; a block walks its run piece by piece, the next piece planned by a
-// warp of its own meanwhile.  See decay_attn.h and decay_attn.cu for the three ways
-// in which a sequence's state gets past the end of a run.
+// warp of its own meanwhile.  decay_attn.h says how a sequence's state gets past the
+// end of a run, decay_attn.cu what that costs.
 //
 // What bounds it (B200, SM clock about 1.75 GHz under load): at 128 x 128 a chunk
 // takes 5700 to 6000 cycles, against 2950 ns x clock = 5200 that its 128 KB take at
 // the SM's share of the measured copy rate and about 3100 of products; the issue
 // slots are half used, and a chunk's chain (mask, dS, update, P v, output) does the
-// rest.  A chunk whose state needs three terms takes 7800, a piece's start 4000, a
-// block's 10000.  At 32 x 64 a chunk takes 8000 in each of two blocks: its chain.
-// Measured whole calls: 16382 packed tokens, 16 heads of 128/128, 124 us (2.3 TB/s);
-// 2 x 12544 tokens, 6 heads of 32/64, 56 us; backward of 4 x 4096 tokens, 16 heads
-// of 128/128, 217 us (2.2 TB/s).
+// rest.  A chunk whose state needs three terms takes 7800, one walked for its state
+// alone 3000, a piece's start 4000, a block's 10000.  At 32 x 64 a chunk takes 8000 in
+// each of two blocks: its chain.  Whole calls: 16382 packed tokens, 16 heads of
+// 128/128, 115 us (2.5 TB/s); 2 x 12544 tokens, 6 heads of 32/64, 54 us; backward of
+// 4 x 4096 tokens, 16 heads of 128/128, 220 us (2.2 TB/s).
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -254,6 +254,11 @@ struct TcCfg {
     if (STATES) return (m & 1) * 192 + 64 * i;
     return i < 2 ? 384 + 64 * i : TM_O1;
   }
+  // the same where only the state is formed, which leaves P and O1 free: two places
+  __device__ static __forceinline__ uint32_t tm_k_state(int m, int i) {
+    if (SMALL || STATES) return tm_k(m, i);
+    return i < 2 ? (m & 1 ? 0 : 384) + 64 * i : TM_O1 + 64 * (m & 1);
+  }
 };
 
 // A piece and what its chunks need of its head's decay.
@@ -295,7 +300,7 @@ struct TcTables {
   int abort;
 };
 
-// STATES: what a block's unfinished unit adds to its state; else a block's outputs, piece by piece.
+// A block's walk through its run, piece by piece; STATES: only what its cut unit adds to its state (the first of two passes).
 // FETCH: how tiles come (one way a kernel: what an SM has to hold of its code counts).
 template <int D, bool STATES, int FETCH>
 __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) decay_tc_kernel(const __grid_constant__ DecayArgs a) {
@@ -334,7 +339,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   }
   // After a first pass (which started after everything before this call had ended) a block plans, fetches its first tiles
   // and waits for that pass only before it touches states.
-  const bool early = !STATES && FETCH != kFetchTokens && a.deal.second;
+  const bool early = !STATES && FETCH != kFetchTokens && a.deal.joined;
   auto depend = [&]() {
     griddep_wait();
     griddep_launch_dependents();
@@ -388,8 +393,9 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         decay_piece(a, per, r1 - 1, r1, u);  // and its last: what the run has of it, unless it ends there
         const bool open = !u.last;
         const long long tail = open ? max(r, u.unit_start) : r1;
-        // walked in full at once where it begins with the unit and the next block can end that
-        const bool once = u.unit_start >= r && u.unit_start + u.unit_chunks <= runs.start(min(me + 2, grid));
+        // walked in full at once where it begins with the unit and the next block ends that, after other work as long
+        const long long end = u.unit_start + u.unit_chunks, next_end = runs.start(min(me + 2, grid));
+        const bool once = u.unit_start >= r && end <= next_end && r1 - tail <= next_end - end + 2;
         if (ln == 0) {
           int i = 4;
           auto put = [&](long long at, long long end, int st, int pub) {
@@ -556,7 +562,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       const uint64_t v0 = mn_desc(tile(1, m), F::ATOM);
 #pragma unroll 1
       for (int i = terms - 1; i >= 0; --i) {  // the smallest terms first
-        const uint32_t ka = tm + F::tm_k(m, i);
+        const uint32_t ka = tm + (state ? F::tm_k_state(m, i) : F::tm_k(m, i));
 #pragma unroll
         for (int ks = 0; ks < C / 16; ++ks)
           mma_ts(one, tm + F::TM_DS, ka + 8 * ks, v0 + (uint64_t)((2048 * ks) >> 4), id_v, ks == 0 && i == terms - 1 ? 0u : 1u);
@@ -897,6 +903,8 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     auto convert_k = [&](int m, int terms, auto last) {
       constexpr bool LAST = decltype(last)::value;
       if (terms == 0) return;
+      const bool at_once = F::THREE_AT_ONCE || state;
+      auto col = [&](int i) { return state ? F::tm_k_state(m, i) : F::tm_k(m, i); };
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         const int c = 32 * (warp & 3) + 16 * half;
@@ -920,15 +928,15 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           const uint32_t at = tmem + (static_cast<uint32_t>(c) << 16) + s0 / 2;
 #pragma unroll
           for (int i = 0; i < 8; ++i) r[i] = take_term(x[i]);
-          if (!LAST) tmem_put_16x16(at + F::tm_k(m, 0), r);
-          if (LAST || (F::THREE_AT_ONCE && terms == 3)) {
+          if (!LAST) tmem_put_16x16(at + col(0), r);
+          if (LAST || (at_once && terms == 3)) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) r[i] = take_term(x[i]);
-            if (!LAST) tmem_put_16x16(at + F::tm_k(m, 1), r);
+            if (!LAST) tmem_put_16x16(at + col(1), r);
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) r[i] = pack2(x[i]);
-          tmem_put_16x16(at + F::tm_k(m, LAST || (F::THREE_AT_ONCE && terms == 3) ? 2 : 1), r);
+          tmem_put_16x16(at + col(LAST || (at_once && terms == 3) ? 2 : 1), r);
         }
       }
       tmem_st_wait();
@@ -1083,6 +1091,25 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       if (!F::SMALL && left > 0) {
         full(base);
         convert_k(base, terms_of(tab, left), kAll);
+      }
+      if (!F::SMALL && state) {
+        // the state alone: khat of the next chunk is formed while the tensor core sums this one's dS
+        arrive(&sh.bar_k);
+#pragma unroll 1
+        for (int m = base; left > 0; ++m, left -= C) {
+          if (__any_sync(0xFFFFFFFFu, timed_out || *reinterpret_cast<volatile int*>(&sh.abort))) break;
+          if (left > C) {
+            full(m + 1);
+            convert_k(m + 1, terms_of(tab, left - C), kAll);
+          }
+          wait_bar(&sh.bar_ds, m & 1);
+          tc_fence_after();
+          update(min(C, left), p.lag && u.t0 == 0 && left == u.n ? 1 : 0);
+          arrive(&sh.bar_p);
+          arrive(FETCH != kFetchTokens ? &sh.bar_out[m & 1] : &sh.free_[1][m % F::ST]);
+          if (left > C) arrive(&sh.bar_k);
+        }
+        left = 0;
       }
 #pragma unroll 1
       for (int m = base; left > 0; ++m, left -= C) {

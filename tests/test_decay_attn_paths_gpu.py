@@ -1,5 +1,5 @@
-"""Head-decay linear attention on the GPU where the work is cut across blocks: states joined by the second pass, by a
-kernel of their own, or handed from block to block; tiles fetched as rows, column runs or token by token."""
+"""Head-decay linear attention on the GPU where the work is cut across blocks: states handed from block to block, or formed
+by a first pass and joined; tiles fetched as rows, column runs or token by token."""
 import pytest
 import torch
 
@@ -13,11 +13,11 @@ HANDED = [
     dict(B=5, H=70, dk=32, dv=8, L=600), dict(B=5, H=70, dk=32, dv=8, grid=(16, 38), mode=3),
     dict(B=5, H=40, dk=72, dv=8, L=600, mode=1), dict(B=4, H=50, dk=8, dv=72, grid=(32, 19), mode=2),
 ]
-# few units, each over many blocks
+# few units, each over several blocks, or over 32 and more
 JOINED = [
     dict(B=1, H=2, dk=32, dv=16, L=4001), dict(B=2, H=1, dk=16, dv=64, grid=(16, 150), mode=3),
     dict(B=1, H=2, dk=72, dv=8, L=3000, mode=1), dict(B=1, H=1, dk=128, dv=128, L=700),
-    dict(B=1, H=2, dk=36, dv=12, L=2500), dict(B=1, H=2, dk=20, dv=68, grid=(19, 70), mode=2),
+    dict(B=1, H=2, dk=36, dv=12, L=2500), dict(B=1, H=1, dk=72, dv=8, L=4200), dict(B=3, H=20, dk=72, dv=8, L=1100, mode=1), dict(B=1, H=2, dk=20, dv=68, grid=(19, 70), mode=2),
 ]
 PACKED = [
     dict(B=4, H=2, dk=32, dv=64, lens=[3000, 5, 0, 900], tail=7), dict(B=4, H=2, dk=32, dv=64, lens=[3000, 5, 0, 900], tail=7, mode=1),
