@@ -12,8 +12,8 @@
 // gradients are summed per thread over the block's rows, then over the block's
 // rows of threads, and the blocks' partial rows by a second kernel, all in a
 // fixed order (no atomics: the same bits from run to run).
-// Forward 16384 x 4096 bf16 48 us (5.6 TB/s, 85% of the measured copy), backward 8191 x 4096 fp32 71 us
-// (5.7 TB/s, 86%); rows that 16-byte vectors do not fit run at 2 to 4 TB/s (a value at a time: the loads'
+// Forward 16384 x 4096 bf16 48 us (5.6 TB/s, 85% of the measured copy), backward 8191 x 4096 fp32 69 us
+// (5.8 TB/s, 89%); rows that 16-byte vectors do not fit run at 2 to 4 TB/s (a value at a time: the loads'
 // and the reductions' latency).
 #include <cuda_bf16.h>
 
@@ -404,11 +404,13 @@ __global__ void __launch_bounds__(kThreads) ln_bwd_wide_kernel(const LnBwdArgs a
   }
 }
 
-// out[c] = sum of the blocks' partial rows: 32 columns per block, eight groups of
-// rows whose sums are added in order.
-__global__ void __launch_bounds__(256) ln_bwd_join_kernel(const float* __restrict__ pw, const float* __restrict__ pb,
+// out[c] = sum of the blocks' partial rows: 32 columns per block, kGroups groups of
+// rows whose sums are added in order.  Its time is a few trips to L2, so groups are
+// many and a thread's loads go out ahead of its additions.
+constexpr int kGroups = 32;
+__global__ void __launch_bounds__(32 * kGroups) ln_bwd_join_kernel(const float* __restrict__ pw, const float* __restrict__ pb,
                                                           float* dw, float* db, int blocks, int D) {
-  __shared__ float part[8][33];
+  __shared__ float part[kGroups][33];
   griddep_wait();
   griddep_launch_dependents();
   const float* p = blockIdx.y ? pb : pw;
@@ -417,13 +419,20 @@ __global__ void __launch_bounds__(256) ln_bwd_join_kernel(const float* __restric
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
-  if (c < D)
-    for (int r = grp; r < blocks; r += 8) s += p[(size_t)r * D + c];
+  if (c < D) {
+    for (int r0 = grp; r0 < blocks; r0 += 5 * kGroups) {
+      float x[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) x[i] = r0 + i * kGroups < blocks ? p[(size_t)(r0 + i * kGroups) * D + c] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 5; ++i) s += x[i];
+    }
+  }
   part[grp][lane] = s;
   __syncthreads();
   if (grp == 0 && c < D) {
 #pragma unroll
-    for (int g = 1; g < 8; ++g) s += part[g][lane];
+    for (int g = 1; g < kGroups; ++g) s += part[g][lane];
     out[c] = s;
   }
 }
@@ -569,7 +578,7 @@ dig_status dig_layer_norm_bwd(const void* x, long long x_stride, const float* we
                                                    : ln_bwd_launch<float, float>(a, vec, s, &blocks));
   }
   if (e == cudaSuccess && par)
-    e = launch_pdl(ln_bwd_join_kernel, dim3((D + 31) / 32, 2), dim3(256), 0, s, a.pw, a.pb, dweight, dbias, blocks, D);
+    e = launch_pdl(ln_bwd_join_kernel, dim3((D + 31) / 32, 2), dim3(32 * kGroups), 0, s, a.pw, a.pb, dweight, dbias, blocks, D);
   return e == cudaSuccess ? DIG_OK : ln_fail(DIG_ERR_CUDA, cudaGetErrorString(e));
 }
 
