@@ -327,6 +327,7 @@ def dig_block_activation(x, kind, stream=None):
 
 # ------------------------------------------------------------------ head-decay attention, layer norm
 _CODES = {torch.float32: DIG_F32, torch.bfloat16: DIG_BF16}
+_F32 = torch.float32
 
 
 def _typed(t):
@@ -340,7 +341,7 @@ def _dense(t, name, shape, dtype, dev):
     """Address of a contiguous tensor of exactly this shape, dtype and device index (None: NULL)."""
     if t is None:
         return None
-    if t.is_contiguous() and t.shape == shape and t.dtype == dtype and t.get_device() == dev:
+    if t.is_contiguous() and t.shape == shape and t.dtype is dtype and t.get_device() == dev:
         return t.data_ptr()
     raise ValueError("%s must be a contiguous %s tensor of shape %s on cuda:%d, got %s %s on %s%s" % (
         name, dtype, tuple(shape), dev, t.dtype, tuple(t.shape), t.device, "" if t.is_contiguous() else ", strided"))
@@ -471,35 +472,42 @@ def dig_decay_attn_bwd(q, k, v, log_decay, dO, dq, dk, dv, workspace, grid_h=Non
 def dig_decay_attn_step(q, k, v, log_decay, S, o, slots=None, scale=1.0, device_status=None, stream=None):
     """One token for each of B sequences: q, k [B,H,dk], v [B,H,dv]; S [n,H,dk,dv] fp32, updated in place (row b uses
     state slots[b], or b); o [B,H,dv].  device_status: optional zeroed int32 [1] (see include/dig.h)."""
-    B, H, dk = q.shape
-    dv = v.shape[2]
-    dev = q.get_device()
-    if k.shape != q.shape or v.shape[:2] != q.shape[:2] or not q.dtype == k.dtype == v.dtype or \
-            not dev == k.get_device() == v.get_device():
+    shape, vshape, dt, dev = q.shape, v.shape, q.dtype, q.get_device()
+    B, H, dk = shape
+    if k.shape != shape or len(vshape) != 3 or vshape[0] != B or vshape[1] != H or k.dtype is not dt or \
+            v.dtype is not dt or k.get_device() != dev or v.get_device() != dev:
         raise ValueError("q, k [B, H, d_k] and v [B, H, d_v] must agree in shape, dtype and device")
-    n = S.shape[0]
+    dv, n = vshape[2], S.shape[0]
     _call(lib.dig_decay_attn_step, "dig_decay_attn_step", dev, stream,
           q.data_ptr(), k.data_ptr(), v.data_ptr(), _tokens(q, "q", H, dk), _tokens(k, "k", H, dk),
-          _tokens(v, "v", H, dv), _dense(log_decay, "log_decay", (H,), torch.float32, dev), scale,
-          _dense(S, "S", (n, H, dk, dv), torch.float32, dev), _dense(slots, "slots", (B,), torch.int32, dev), n,
-          _dense(o, "o", v.shape, o.dtype, dev), B, H, dk, dv, _typed(q), _typed(o),
+          _tokens(v, "v", H, dv), _dense(log_decay, "log_decay", (H,), _F32, dev), scale,
+          _dense(S, "S", (n, H, dk, dv), _F32, dev), _dense(slots, "slots", (B,), torch.int32, dev), n,
+          _dense(o, "o", vshape, o.dtype, dev), B, H, dk, dv, _typed(q), _typed(o),
           _dense(device_status, "device_status", (1,), torch.int32, dev))
+
+
+def _rows(x):
+    """(D, rows, elements between rows) of x [..., D], whose rows must be dense and one stride apart."""
+    shape = x.shape
+    if not shape or shape[-1] == 0:
+        raise ValueError("x must be [..., D] with dense rows")
+    D = shape[-1]
+    if x.is_contiguous():
+        return D, x.numel() // D, D
+    if D > 1 and x.stride(-1) != 1:
+        raise ValueError("x must be [..., D] with dense rows")
+    return D, x.numel() // D, _row_stride(x, "x", 1, D)
 
 
 def dig_layer_norm_fwd(x, y, weight=None, bias=None, eps=1e-5, mean=None, rstd=None, stream=None):
     """y = (x - mean) * rstd * weight + bias over the last dimension; x [..., D] (rows one stride apart), y dense;
     weight, bias [D] fp32; mean, rstd [rows] fp32 outputs."""
-    D = x.shape[-1]
+    D, rows, stride = _rows(x)
     dev = x.get_device()
-    if x.dim() < 1 or D == 0 or (D > 1 and x.stride(-1) != 1):
-        raise ValueError("x must be [..., D] with dense rows")
-    rows = x.numel() // D
-    f32 = torch.float32
     _call(lib.dig_layer_norm_fwd, "dig_layer_norm_fwd", dev, stream,
-          x.data_ptr(), _row_stride(x, "x", 1, D), _dense(weight, "weight", (D,), f32, dev),
-          _dense(bias, "bias", (D,), f32, dev), eps, _dense(y, "y", x.shape, y.dtype, dev),
-          _dense(mean, "mean", (rows,), f32, dev), _dense(rstd, "rstd", (rows,), f32, dev), rows, D, _typed(x),
-          _typed(y))
+          x.data_ptr(), stride, _dense(weight, "weight", (D,), _F32, dev), _dense(bias, "bias", (D,), _F32, dev), eps,
+          _dense(y, "y", x.shape, y.dtype, dev), _dense(mean, "mean", (rows,), _F32, dev),
+          _dense(rstd, "rstd", (rows,), _F32, dev), rows, D, _typed(x), _typed(y))
 
 
 def new_layer_norm_workspace(rows, D, device="cuda") -> torch.Tensor:
@@ -510,17 +518,13 @@ def new_layer_norm_workspace(rows, D, device="cuda") -> torch.Tensor:
 def dig_layer_norm_bwd(x, dy, mean, rstd, dx, weight=None, dw=None, db=None, workspace=None, stream=None):
     """Gradients for dig_layer_norm_fwd: x as there, dy, dx dense and like x; mean, rstd [rows] of the forward; dw, db
     [D] fp32 (either needs the workspace)."""
-    D = x.shape[-1]
+    D, rows, stride = _rows(x)
     dev = x.get_device()
-    if x.dim() < 1 or D == 0 or (D > 1 and x.stride(-1) != 1):
-        raise ValueError("x must be [..., D] with dense rows")
-    rows = x.numel() // D
-    f32 = torch.float32
     _call(lib.dig_layer_norm_bwd, "dig_layer_norm_bwd", dev, stream,
-          x.data_ptr(), _row_stride(x, "x", 1, D), _dense(weight, "weight", (D,), f32, dev),
-          _dense(mean, "mean", (rows,), f32, dev), _dense(rstd, "rstd", (rows,), f32, dev),
+          x.data_ptr(), stride, _dense(weight, "weight", (D,), _F32, dev),
+          _dense(mean, "mean", (rows,), _F32, dev), _dense(rstd, "rstd", (rows,), _F32, dev),
           _dense(dy, "dy", x.shape, x.dtype, dev), _dense(dx, "dx", x.shape, dx.dtype, dev),
-          _dense(dw, "dw", (D,), f32, dev), _dense(db, "db", (D,), f32, dev), rows, D, _typed(x), _typed(dx),
+          _dense(dw, "dw", (D,), _F32, dev), _dense(db, "db", (D,), _F32, dev), rows, D, _typed(x), _typed(dx),
           None if workspace is None else _dense(workspace, "workspace", workspace.shape, torch.uint8, dev),
           0 if workspace is None else workspace.numel())
 
