@@ -1,6 +1,6 @@
 // decay_attn.h -- what the kernels of the head-decay linear attention share:
-// the problems of one call, how a sequence is cut into segments, and the walk
-// from a block to its segment.
+// the problems of one call, how they are cut up among blocks, and the walk from a
+// block to its part.
 //
 // A problem is  o_t = c lambda^(t+1) q_t S0 + a sum_{s<=t} lambda^(t-s) (q_t . k_s) v_s
 // over scan positions t of a sequence, with the carried state
@@ -11,10 +11,11 @@
 // adjoint one, starts from dS_final (transposed for dk) without the first lambda
 // ("lag"), and ends, times lambda, as dS0.
 //
-// A sequence is cut into segments of `seg` tokens, each walked by one block in
-// chunks.  With more than one segment per sequence a first kernel leaves every
-// segment's own state contribution (segment 0: with S0 in it), and the second
-// one joins those before its segment into the state it starts from.
+// On the FP32 pipes a sequence is cut into segments of `seg` tokens, each walked by
+// one block in chunks.  With more than one segment per sequence a first kernel leaves
+// every segment's own state contribution (segment 0: with S0 in it), and the second
+// one joins those before its segment into the state it starts from.  How the
+// tensor-core kernel does it is at DecayDeal.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>

@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     griddep_launch_dependents();
   };
   if (!early) depend();
-  if (FETCH != kFetchTokens && warp == W0 + 1 && ln < 7)
+  if (FETCH != kFetchTokens && warp == W0 + 1 && (ln < 4 ? ln < 3 || a.deal.nprob > 1 : ln - 4 < a.deal.nprob))
     asm volatile("prefetch.tensormap [%0];" ::"l"(tmap_addr(ln < 4 ? a.map[ln] : a.omap[ln - 4])) : "memory");
   if (!STATES && a.cu && blockIdx.x == 0 && warp == 0) decay_check_offsets(a);
   bool on = true;

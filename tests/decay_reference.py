@@ -59,11 +59,10 @@ def attn_bound(size, longest, dk, dv, bf16):
 
     Every output is a sum of products q k v lambda^n.  A chain of at most dk + dv + 2 longest + 64 roundings of
     2^-23 at most (a tensor-core addition may cut instead of rounding; the decays cost a few more) leads to it.
-    With bf16 inputs and outputs the masked products, the state and the decayed keys enter their second product
-    rounded to bf16, the way the output leaves: a term meets one of the first two and at most one of the third, each
-    off by at most UBF of it."""
+    With bf16 inputs and outputs the state enters its product with q rounded to bf16, the way the output leaves: off by
+    at most UBF.  The masked products and the decayed keys enter theirs as two bf16 terms, off by at most UBF^2 each."""
     c = (dk + dv + 2 * longest + 64) * 2 * U32
-    return (c + (2 * UBF + UBF * UBF if bf16 else 0.0)) * size
+    return (c + (UBF + 3 * UBF * UBF if bf16 else 0.0)) * size
 
 
 def layer_norm(x, w, b, eps):

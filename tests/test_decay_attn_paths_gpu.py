@@ -126,3 +126,46 @@ def test_captured_and_replayed_backward():
                 x.zero_()
             graph.replay()
             assert all(torch.equal(x, w) for x, w in zip((*outs, dS0), want))
+
+
+def test_training_step_of_norm_and_attention():
+    """Layer norm -> fused q, k, v slices -> attention, and back through both, against automatic differentiation in 64 bits."""
+    dig = _dig()
+    B, L, H, dk, dv = 2, 150, 3, 32, 64
+    D = H * (2 * dk + dv)
+    gen = torch.Generator().manual_seed(5)
+    x = torch.randn(B, L, D, generator=gen)
+    w, b = 0.2 + 0.05 * torch.randn(D, generator=gen), 0.05 * torch.randn(D, generator=gen)
+    g = -torch.exp2(-2.0 * torch.arange(1, H + 1))
+    dO = torch.randn(B, L, H, dv, generator=gen)
+
+    xr, wr, br = (t.double().requires_grad_() for t in (x, w, b))
+    q, k, v = torch.nn.functional.layer_norm(xr, (D,), wr, br, 1e-5).split([H * dk, H * dk, H * dv], -1)
+    q, k, v = q.unflatten(-1, (H, dk)), k.unflatten(-1, (H, dk)), v.unflatten(-1, (H, dv))
+    S, outs = torch.zeros(B, H, dk, dv, dtype=torch.float64), []
+    for t in range(L):
+        S = torch.exp(g.double())[:, None, None] * S + k[:, t, :, :, None] * v[:, t, :, None, :]
+        outs.append(torch.einsum("bhk,bhkv->bhv", q[:, t], S))
+    want_o = torch.stack(outs, 1)
+    (want_o * dO.double()).sum().backward()
+
+    xd, wd, bd, gd, dOd = (t.cuda() for t in (x, w, b, g, dO))
+    y, mean, rstd = torch.empty_like(xd), torch.empty(B * L, device="cuda"), torch.empty(B * L, device="cuda")
+    dig.dig_layer_norm_fwd(xd, y, weight=wd, bias=bd, mean=mean, rstd=rstd)
+    sizes = [H * dk, H * dk, H * dv]
+    qkv = [p.unflatten(-1, (H, d)) for p, d in zip(y.split(sizes, -1), (dk, dk, dv))]
+    o = torch.empty(B, L, H, dv, device="cuda")
+    ws = dig.new_decay_attn_workspace(B, H, L, dk, dv, dtype=torch.float32)
+    dig.dig_decay_attn_fwd(*qkv, gd, o, ws)
+    grads = [torch.empty(B, L, H, d, device="cuda") for d in (dk, dk, dv)]
+    wsb = dig.new_decay_attn_workspace(B, H, L, dk, dv, dtype=torch.float32, backward=True)
+    dig.dig_decay_attn_bwd(*qkv, gd, dOd, *grads, wsb)
+    dy = torch.cat([t.flatten(-2) for t in grads], -1)
+    dx, dw, db = torch.empty_like(xd), torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    dig.dig_layer_norm_bwd(xd, dy, mean, rstd, dx, weight=wd, dw=dw, db=db, workspace=dig.new_layer_norm_workspace(B * L, D))
+    # chains of at most dk + dv + L + D additions of fp32 values, whose roundings add up like random numbers do: the root of
+    # their number times 2^-24, times four for the four operators in a row
+    bound = 4 * (dk + dv + L + D) ** 0.5 * 2.0 ** -24
+    for got, want in ((o, want_o), (dx, xr.grad), (dw, wr.grad), (db, br.grad)):
+        want = want.detach()
+        assert (got.double().cpu() - want).norm() <= bound * want.norm()
