@@ -344,19 +344,9 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     griddep_wait();
     griddep_launch_dependents();
   };
-  if (!early) depend();
   if (FETCH != kFetchTokens && warp == W0 + 1 && (ln < 4 ? ln < 3 || a.deal.nprob > 1 : ln - 4 < a.deal.nprob))
     asm volatile("prefetch.tensormap [%0];" ::"l"(tmap_addr(ln < 4 ? a.map[ln] : a.omap[ln - 4])) : "memory");
-  if (!STATES && a.cu && blockIdx.x == 0 && warp == 0) decay_check_offsets(a);
-  bool on = true;
-  if (sb & 1023u) {  // the swizzled tiles start at 1024-byte boundaries
-    if (tid == 0) set_status(a.status, DIG_ERR_CUDA);
-    on = false;
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh.tmem;
+  const bool on = (sb & 1023u) == 0;  // the swizzled tiles start at 1024-byte boundaries
   // Waits are bounded; after one gave up every other one does, nothing more is issued and the block leaves.
   bool timed_out = false;
   auto wait_bar = [&](uint64_t* bar, uint32_t parity) {
@@ -365,6 +355,8 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     return !timed_out;
   };
 
+  // Where the first piece follows from the arguments alone, it is planned while the kernels before this one end.
+  const bool planned = !a.cu && !a.slots && !a.deal.handoff;
   // Every role walks the pieces, parted by block-wide barriers; one warp plans the next while this one is walked.
   auto plan = [&](int k) {
     TcPiece& t = sh.piece[k & 1];
@@ -439,7 +431,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       if (STATES) more = !u.last;
       if (ln == 0) {
         t.u = u;
-        t.g = a.g[u.h];
+        if (k > 0 || !planned) t.g = a.g[u.h];
         t.keep = a.p[u.z].Sf && u.slot >= 0;
         t.j0 = a.deal.joined ? me - 1 : runs.block_of(u.unit_start);
         t.state = state;
@@ -486,8 +478,16 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       if (j < 32) t.pa[j] = p.a * w.x;
     }
   };
+  if (!early && !planned) depend();
   if (warp == W0 + 3) plan(0);
+  if (!early && planned) depend();
+  if (!on && tid == 0) set_status(a.status, DIG_ERR_CUDA);
+  if (!STATES && a.cu && blockIdx.x == 0 && warp == 0) decay_check_offsets(a);
+  if (planned && warp == W0 + 3 && ln == 0 && sh.piece[0].more) sh.piece[0].g = a.g[sh.piece[0].u.h];
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
   if (tid < NT) powers(sh.piece[0], tid, NT);
   __syncthreads();
   // Every role is through with the piece; false: one gave up.
