@@ -5,7 +5,7 @@
 // (row, head) holds up to 64 rows' worth of 16-byte loads per column group in
 // flight: thread = (4 value channels, one of RL key-channel lanes), 16 key rows
 // of a lane at a time in registers.  Everything is fp32; only o is rounded.
-// 253 rows, 16 heads of 128/128 (535 MB): 87.7 us, 6.1 TB/s, 93% of the measured copy;
+// 253 rows, 16 heads of 128/128 (535 MB): 85 to 88 us, 6.1 TB/s, 93% of the measured copy;
 // one row of 6 heads of 32/64: 4.3 us on the device, a launch's time.
 #include <cuda_bf16.h>
 

@@ -353,7 +353,8 @@ dig_status dig_block_activation(void *x, long long n, int kind, void *stream);
  * device: a bad offset (clamped to its range), a slot of n_slots or more or one that an
  * earlier sequence has (then taken as negative) sets DIG_ERR_INVALID_ARGUMENT in the
  * workspace's status word.  The workspace (dig_decay_attn_workspace_bytes, zero-filled
- * before the first use, and again after DIG_ERR_DEVICE_TIMEOUT) is scratch of one call at a time.  Results do not depend on
+ * before the first use, and again after DIG_ERR_DEVICE_TIMEOUT) is scratch of one call at a time.  o overlaps no input
+ * (blocks read tokens that others have answered).  Results do not depend on
  * what shares the call and are the same from run to run. */
 dig_status dig_decay_attn_fwd(const void *q, const void *k, const void *v, long long q_stride,
                               long long k_stride, long long v_stride, const float *log_decay, float scale,
@@ -368,7 +369,7 @@ dig_status dig_decay_attn_fwd(const void *q, const void *k, const void *v, long 
  *   dS_final   [B, H, d_k, d_v] fp32 or NULL (zero)
  *   dq, dk     [rows, H, d_k] out_dtype;  dv [rows, H, d_v] out_dtype; dense; rows of no
  *              sequence are left as they were
- *   dS0        [B, H, d_k, d_v] fp32 or NULL: the gradient of S0
+ *   dS0        [B, H, d_k, d_v] fp32 or NULL: the gradient of S0; it overlaps no input
  * Nothing of the forward is kept: the states are computed again. */
 dig_status dig_decay_attn_bwd(const void *q, const void *k, const void *v, long long q_stride,
                               long long k_stride, long long v_stride, const float *log_decay, float scale,
