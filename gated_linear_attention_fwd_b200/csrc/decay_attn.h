@@ -112,7 +112,10 @@ __device__ __forceinline__ int decay_slot(const DecayArgs& a, int b) {
 }
 
 // The unit of segment slot `sidx` of the call; every lane of the calling warp
-// gets it.  False: the call has fewer segments.
+// gets it.  False: the call has fewer segments, or the unit's sequence reaches past
+// the call's slots, one per block of gridDim.x.  Only sequences that overlap, as
+// those of descending offsets do, can: they come to more tokens than the rows that
+// the slots are counted for, and are left out whole.
 __device__ __forceinline__ bool decay_unit(const DecayArgs& a, int sidx, DecayUnit& u) {
   const int lane = threadIdx.x & 31;
   if (!a.cu) {
@@ -148,7 +151,7 @@ __device__ __forceinline__ bool decay_unit(const DecayArgs& a, int sidx, DecayUn
       }
       base += __shfl_sync(0xFFFFFFFFu, inc, 31);
     }
-    if (!found) return false;
+    if (!found || sidx - u.i + u.nseg > (int)gridDim.x) return false;
   }
   u.t0 = u.i * a.seg;
   u.n = min(a.seg, u.len - u.t0);

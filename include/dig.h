@@ -350,9 +350,10 @@ dig_status dig_block_activation(void *x, long long n, int kind, void *stream);
  * d_k and d_v are multiples of 4 up to 128, strides multiples of 4 elements; else
  * DIG_ERR_UNSUPPORTED.  q, k and v are aligned to four elements, the rest to 16 bytes.  Values have to be finite: a NaN or infinity may reach other
  * tokens of its own sequence (never another sequence's).  Offsets and slots live on the
- * device: a bad offset (clamped to its range), a slot of n_slots or more or one that an
- * earlier sequence has (then taken as negative) sets DIG_ERR_INVALID_ARGUMENT in the
- * workspace's status word.  The workspace (dig_decay_attn_workspace_bytes, zero-filled
+ * device: offsets that leave 0 .. L or descend (clamped to the rows; what such a call leaves
+ * in o and S_final is undefined, and some of it may not be written), a slot of n_slots or
+ * more or one that an earlier sequence has (then taken as negative) set
+ * DIG_ERR_INVALID_ARGUMENT in the workspace's status word.  The workspace (dig_decay_attn_workspace_bytes, zero-filled
  * before the first use, and again after DIG_ERR_DEVICE_TIMEOUT) is scratch of one call at a time.  o overlaps no input
  * (blocks read tokens that others have answered).  Results do not depend on
  * what shares the call and are the same from run to run. */
