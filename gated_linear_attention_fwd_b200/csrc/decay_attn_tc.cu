@@ -1118,9 +1118,16 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         const int e = (p.lag && u.t0 == 0 && left == u.n) ? 1 : 0;
         const int terms = terms_of(tab, left);
         if (F::SMALL) full(m);
-        // khat (D = 128: its third term) comes over the last chunk's outputs, once the warps of these lanes have read them
+        // khat (D = 128: its third term) comes over the last chunk's outputs, once the warps of these lanes have read them.
+        // At D = 64 all of them leave together there.  At D = 128 only chunks of three terms have that barrier, and after a
+        // wait was given up the warps may learn of it on different sides of the first one: the chunks that are left are
+        // passed over, their barriers are not.
         const bool stop = timed_out || *reinterpret_cast<volatile int*>(&sh.abort);
-        if (F::SMALL || terms == 3 ? bar_or(1 + (warp & 3), 32 * CG, stop) : (bool)__any_sync(0xFFFFFFFFu, stop)) break;
+        if (F::SMALL || terms == 3 ? bar_or(1 + (warp & 3), 32 * CG, stop) : (bool)__any_sync(0xFFFFFFFFu, stop)) {
+          if (F::SMALL) break;
+          timed_out = true;
+          continue;
+        }
         if (F::SMALL) convert_k(m, terms, kAll);
         else if (terms == 3) convert_k(m, terms, kThird);
         arrive(&sh.bar_k);
