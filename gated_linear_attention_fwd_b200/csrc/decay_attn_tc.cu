@@ -490,10 +490,13 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   const uint32_t tmem = sh.tmem;
   if (tid < NT) powers(sh.piece[0], tid, NT);
   __syncthreads();
-  // Every role is through with the piece; false: one gave up.
+  // Every role is through with the piece; false: one gave up.  The second barrier keeps the others from the next piece's
+  // waits until all have read the flag: put up by one of those, it would part roles that have read it from those that have not.
   auto piece_done = [&]() {
     named_bar(0, NT + 128);
-    return *reinterpret_cast<volatile int*>(&sh.abort) == 0;
+    const bool gone = *reinterpret_cast<volatile int*>(&sh.abort) != 0;
+    named_bar(0, NT + 128);
+    return !gone;
   };
   auto tile = [&](int x, int m) { return sb + ((m % F::ST) * F::PER + x) * F::TILE; };  // x: 0 k, 1 v, 2 q
   // a value that every lane has, as one the compiler knows to be the same in all of them

@@ -59,3 +59,37 @@ def test_workers_that_left_their_loop_would_not():
     """Leaving is safe only where every chunk has the vote (heads of up to 64 channels), or none."""
     assert workers_end([2, 2, 2], leaves=True) and workers_end([3, 3, 3], leaves=True)
     assert not workers_end([2, 2, 3], leaves=True)
+
+
+# ------------------------------------------------------------------ all roles, piece by piece
+def role(pieces, gives_up, flag, late, barriers):
+    """One role's barriers: those at the end of each piece, then the block's.  gives_up: the piece in which it puts up the
+    flag; late: with one barrier a piece, whether it reads the flag only when others are through the next piece's waits."""
+    for i in range(pieces):
+        if i == gives_up:
+            flag.add(i)
+        yield PIECE
+        gone = any(j <= i + (late and barriers == 1) for j in flag)
+        if barriers == 2:
+            yield PIECE
+        if gone:
+            break
+    yield PIECE
+
+
+def roles_end(barriers):
+    """Three roles, each giving up in any piece or never, and reading early or late."""
+    for gives in seen(3, 3):
+        for late in itertools.product((False, True), repeat=3):
+            flag = set(gives) - {3}
+            if not run([role(3, g, flag, x, barriers) for g, x in zip(gives, late)], {PIECE: 3}):
+                return False
+    return True
+
+
+def test_roles_leave_at_the_same_piece():
+    assert roles_end(barriers=2)
+
+
+def test_roles_with_one_barrier_a_piece_would_not():
+    assert not roles_end(barriers=1)
