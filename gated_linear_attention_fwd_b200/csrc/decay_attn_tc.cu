@@ -635,9 +635,14 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       }
       __syncwarp();
     };
-    auto freed = [&](int x, int m) {  // the place of tile x of chunk m
-      return m < F::ST || __all_sync(0xFFFFFFFFu, wait_bar(&sh.free_[x][m % F::ST], (m / F::ST - 1) & 1));
+    // The place of tile x of chunk m is free; nothing more is fetched once a wait was given up (the others' signals need
+    // not mean what they say then).
+    auto freed = [&](int x, int m) {
+      return m < F::ST || __all_sync(0xFFFFFFFFu, wait_bar(&sh.free_[x][m % F::ST], (m / F::ST - 1) & 1) &&
+                                                      *reinterpret_cast<volatile int*>(&sh.abort) == 0);
     };
+    int asked = F::PER * end;  // tiles asked for by the piece's end, F::PER a chunk: k, q, v
+    bool unclean = false;      // the last of those chunks is yet to be cleaned
     if constexpr (FETCH != kFetchTokens) {
       // one warp asks for a chunk's tiles in the order in which their places become free, one stores outputs, one plans
       if (warp == W0 + 1) {
@@ -671,20 +676,31 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
           // packed: rows past the sequence's end are another's, and 0 times them need not be 0
           const bool clean = a.cu && n < C;
           if (due && m == 2) depend(), due = false;
-          if (!freed(0, m)) break;
+          if (!freed(0, m)) {
+            asked = F::PER * m;
+            break;
+          }
           weights(m, n);
           fetch(0, m, clean);
           if (!STATES) {
-            if (!freed(2, m)) break;
+            if (!freed(2, m)) {
+              asked = F::PER * m + 1, unclean = clean;
+              break;
+            }
             if (!tab.state) fetch(2, m, false);
             else if (ln == 0) mbar_arrive(&sh.full[2][m % F::ST]);  // nothing reads q
           }
-          if (!freed(1, m)) break;
+          if (!freed(1, m)) {
+            asked = F::PER * m + F::PER - 1, unclean = clean;
+            break;
+          }
           fetch(1, m, clean);
           if (clean) {
+            bool ok = true;
 #pragma unroll 1
             for (int x = 0; x < 2; ++x) {
-              wait_bar(&sh.landed[x], cleaned & 1);
+              ok = __all_sync(0xFFFFFFFFu, ok && wait_bar(&sh.landed[x], cleaned & 1));
+              if (!ok) break;
               const int r0 = rev ? 0 : n, atoms = min(D / 64, ((x == 1 ? p.dv : p.dk) + 63) / 64);
 #pragma unroll 1
               for (int i = ln; i < (C - n) * 8; i += 32)
@@ -692,6 +708,10 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
               fence_async_smem();
               __syncwarp();
               if (ln == 0) mbar_arrive(&sh.full[x][m % F::ST]);
+            }
+            if (!ok) {
+              asked = F::PER * (m + 1), unclean = true;
+              break;
             }
             ++cleaned;
           }
@@ -703,7 +723,8 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         const int atoms = (p.dv + 63) / 64;
 #pragma unroll 1
         for (int m = base; m < end; ++m) {
-          if (!__all_sync(0xFFFFFFFFu, wait_bar(&sh.bar_out[m & 1], (m >> 1) & 1))) break;
+          if (!__all_sync(0xFFFFFFFFu, wait_bar(&sh.bar_out[m & 1], (m >> 1) & 1) &&
+                                           *reinterpret_cast<volatile int*>(&sh.abort) == 0)) break;
           const int t0 = u.t0 + (m - base) * C;
           if (ln == 0) {
             if (u.n - (m - base) * C >= C && !tab.state) {
@@ -778,9 +799,21 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       }
     }
     base = end;
-    if (!piece_done()) break;
+    if (!piece_done()) {
+      // No load outlives the block: the last one into each place (all of them, were it not for the giving up, are waited for
+      // by the warps that read them).
+      if (FETCH != kFetchTokens && warp == W0 + 1) {
+#pragma unroll 1
+        for (int i = max(asked - F::PER * F::ST, 0); i < asked; ++i) {
+          const int m = i / F::PER, x = i % F::PER == 0 ? 0 : (i % F::PER == F::PER - 1 ? 1 : 2);
+          const bool landed = unclean && m == (asked - 1) / F::PER && x < 2;
+          mbar_wait(landed ? &sh.landed[x] : &sh.full[x][m % F::ST], (landed ? cleaned : m / F::ST) & 1, kSpinLimitNs);
+        }
+      }
+      break;
     }
-    if (!STATES && FETCH != kFetchTokens && warp == W0 + 2) bulk_wait_all();  // no store outlives the block
+    }
+    if (!STATES && FETCH != kFetchTokens && warp == W0 + 2) bulk_wait_all();  // nor does a store
   } else {
     // ---- the workers
     regs_up<F::WORKER_REGS>();

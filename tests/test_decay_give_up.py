@@ -93,3 +93,53 @@ def test_roles_leave_at_the_same_piece():
 
 def test_roles_with_one_barrier_a_piece_would_not():
     assert not roles_end(barriers=1)
+
+
+# ------------------------------------------------------------------ the loads that a block leaves behind
+def fetches(pieces, per, st, stop):
+    """The fetching warp's loads, as (barrier, phase) in order, up to the step at which it gives up, and what it keeps of
+    them: (loads, tiles asked for, cleaned pieces, whether the last chunk is yet to be cleaned).  pieces: (chunks, whether
+    the last one is cleaned after it landed)."""
+    loads, asked, cleaned, unclean, m, step = [], 0, 0, False, 0, 0
+    for chunks, ends_inside in pieces:
+        for i in range(chunks):
+            clean = ends_inside and i == chunks - 1
+            for x in ([0, 2, 1] if per == 3 else [0, 1]):
+                if step == stop:
+                    return loads, asked, cleaned, unclean
+                step += 1
+                if x == 0:
+                    unclean = clean
+                asked += 1
+                loads.append((("landed", x), cleaned) if clean and x < 2 else (("full", x, m % st), m // st))
+            if clean:
+                for x in (0, 1):
+                    if step == stop:
+                        return loads, asked, cleaned, unclean
+                    step += 1
+                unclean, cleaned = False, cleaned + 1
+            m += 1
+    return loads, asked, cleaned, unclean
+
+
+@pytest.mark.parametrize("per, st", [(2, 3), (3, 2)])
+def test_a_block_that_gives_up_waits_for_its_loads(per, st):
+    """The barriers it waits for in the end cover the last load into every place (those before have been waited for by the
+    warps that freed the place), in the phase of that load."""
+    for pieces in itertools.product([(1, False), (1, True), (2, True), (5, False), (4, True)], repeat=3):
+        steps = sum(per * n + 2 * c for n, c in pieces)
+        for stop in range(steps + 1):
+            loads, asked, cleaned, unclean = fetches(pieces, per, st, stop)
+            waits = set()
+            for i in range(max(asked - per * st, 0), asked):
+                m, x = i // per, 0 if i % per == 0 else (1 if i % per == per - 1 else 2)
+                landed = unclean and m == (asked - 1) // per and x < 2
+                waits.add((("landed", x), cleaned) if landed else (("full", x, m % st), m // st))
+            for (bar, phase), n in zip(loads, itertools.count()):
+                if n < asked - per * st or (bar[0] == "landed" and phase < cleaned):
+                    continue    # its place was freed since, or it was waited for before it was cleaned
+                assert (bar, phase) in waits, (pieces, stop, bar, phase)
+            # a barrier waited for in vain would hold the block up for two seconds: each has its load, or was signalled
+            signalled = {(("full", x, m % st), m // st) for m in range(asked // per + 1) for x in (0, 1)}
+            assert all(w in set(loads) or (w in signalled and not (unclean and w[0][1] < 2 and w[1] * st + w[0][2] == (asked - 1) // per))
+                       for w in waits)
