@@ -11,6 +11,7 @@
 namespace dig {
 
 void set_last_error(const char* msg);       // dig_api.cu
+unsigned long long spin_limit_ns();         // dig_api.cu
 
 namespace {
 
@@ -205,6 +206,9 @@ dig_status launch(DecayArgs& a, int nprob, int dk, int dv, void* ws, int dtype, 
     a.deal = d.d;
     a.flag = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + sizeof(WsHeader));
     a.counter = static_cast<WsHeader*>(ws)->pad;
+    const unsigned long long limit = spin_limit_ns();
+    a.short_wait = limit != 0 && limit < kSpinLimitNs;
+    a.late_chunk = limit < 1000 ? (int)limit - 1 : -1;
     e = launch_decay_tc(a, d.multi, d.D, s);
   } else {
     const Cut c = cut_for(a.B, a.H, a.L, dk, dv, a.cu != nullptr, nprob);

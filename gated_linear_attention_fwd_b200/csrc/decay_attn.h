@@ -76,6 +76,9 @@ struct DecayArgs {
   float* segst;   // tensor core: [2][block][D * D], what a block's cut unit adds to its state, and the copy of its S0; else [problem][segment][H][D * D] segment states
   long long segst_problem;  // elements between problems there
   uint32_t* status;
+  // The tensor core's waits: whether a limit below the default holds, which has passed after some 0.1 ms, and the chunk of
+  // a block whose loads are made to outlast it (-1: none).
+  int short_wait, late_chunk;
 };
 
 struct DecayUnit {

@@ -201,22 +201,32 @@ __device__ __forceinline__ uint32_t elect_one() {
   return r;
 }
 
-// Probes until the phase completes, another warp has given up, or the limit has passed (then sets *abort).  The flag
-// and the timer are looked at once in 32 probes: the warps that wait share their issue slots with those that work.
+// The low half of the timer: waits end within its four seconds.
+__device__ __forceinline__ uint32_t timer_ns() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+// What sh.abort holds: a wait was given up; the call's limit is a short one (a test's).
+enum { kGone = 1, kShort = 2 };
+__device__ __forceinline__ bool gone(const int* abort) { return (*reinterpret_cast<const volatile int*>(abort) & kGone) != 0; }
+// After a first probe that failed: probes until the phase completes, another warp has given up, or the limit has passed
+// (then gives up).  The flag and the timer are looked at once in 32 probes, each of which suspends the thread for up to
+// 4 us: the warps that wait share their issue slots with those that work.  A short limit has passed with the first 32.  (The
+// limit itself as an operand of these loops costs the workers registers: 16384 tokens of 16 heads of 36/72 226 us, so 211.)
 __device__ __forceinline__ bool mbar_wait_or(uint64_t* bar, uint32_t parity, int* abort) {
-  uint64_t t0 = 0;
+  uint32_t t0 = 0;
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 32; ++i)
       if (mbar_try_wait(bar, parity)) return true;
-    if (*reinterpret_cast<volatile int*>(abort)) return false;
-    const uint64_t now = globaltimer_ns();
+    if (*reinterpret_cast<volatile int*>(abort)) break;
+    const uint32_t now = timer_ns();
     if (t0 == 0) t0 = now;
-    if (now - t0 > kSpinLimitNs) {
-      *reinterpret_cast<volatile int*>(abort) = 1;
-      return false;
-    }
+    if (now - t0 > (uint32_t)kSpinLimitNs) break;
   }
+  *reinterpret_cast<volatile int*>(abort) = kGone | kShort;
+  return false;
 }
 
 // Second operand read MN-major: rows are the contracted index, atoms of 64 columns `atom` bytes apart.
@@ -334,7 +344,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     mbar_init(&sh.bar_end, 1);
     mbar_init(&sh.landed[0], 1);
     mbar_init(&sh.landed[1], 1);
-    sh.abort = 0;
+    sh.abort = a.short_wait ? kShort : 0;
     fence_mbar_init();
   }
   // After a first pass (which started after everything before this call had ended) a block plans, fetches its first tiles
@@ -347,7 +357,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   if (FETCH != kFetchTokens && warp == W0 + 1 && (ln < 4 ? ln < 3 || a.deal.nprob > 1 : ln - 4 < a.deal.nprob))
     asm volatile("prefetch.tensormap [%0];" ::"l"(tmap_addr(ln < 4 ? a.map[ln] : a.omap[ln - 4])) : "memory");
   const bool on = (sb & 1023u) == 0;  // the swizzled tiles start at 1024-byte boundaries
-  // Waits are bounded; after one gave up every other one does, nothing more is issued and the block leaves.
+  // Waits are bounded by the call's limit; after one gave up every other one does, nothing more is issued and the block leaves.
   bool timed_out = false;
   auto wait_bar = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -494,9 +504,9 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   // waits until all have read the flag: put up by one of those, it would part roles that have read it from those that have not.
   auto piece_done = [&]() {
     named_bar(0, NT + 128);
-    const bool gone = *reinterpret_cast<volatile int*>(&sh.abort) != 0;
+    const bool leave = gone(&sh.abort);
     named_bar(0, NT + 128);
-    return !gone;
+    return !leave;
   };
   auto tile = [&](int x, int m) { return sb + ((m % F::ST) * F::PER + x) * F::TILE; };  // x: 0 k, 1 v, 2 q
   // a value that every lane has, as one the compiler knows to be the same in all of them
@@ -509,16 +519,16 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
   };
   // Waits, as long as wait_bar would, for another block's flag.
   auto wait_flag = [&](const uint32_t* f) {
-    uint64_t t0 = 0;
+    uint32_t t0 = 0;
     while (true) {
       uint32_t v;
       asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(f) : "memory");
-      if (v || timed_out || *reinterpret_cast<volatile int*>(&sh.abort)) return;
-      const uint64_t now = globaltimer_ns();
+      if (v || timed_out || gone(&sh.abort)) return;
+      const uint32_t now = timer_ns();
       if (t0 == 0) t0 = now;
-      if (now - t0 > kSpinLimitNs) {
+      if (now - t0 > (a.short_wait ? 100000u : (uint32_t)kSpinLimitNs)) {
         timed_out = true;
-        sh.abort = 1;
+        sh.abort = kGone | kShort;
       }
     }
   };
@@ -639,7 +649,12 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
     // not mean what they say then).
     auto freed = [&](int x, int m) {
       return m < F::ST || __all_sync(0xFFFFFFFFu, wait_bar(&sh.free_[x][m % F::ST], (m / F::ST - 1) & 1) &&
-                                                      *reinterpret_cast<volatile int*>(&sh.abort) == 0);
+                                                      (FETCH == kFetchTokens || !gone(&sh.abort)));
+    };
+    // A test's: the v tile of this chunk of a block comes only after the others have given up (or a millisecond).
+    auto late = [&](int m) {
+      if (m != a.late_chunk) return;
+      for (const uint32_t t0 = timer_ns(); !gone(&sh.abort) && timer_ns() - t0 < 1000000u;) {}
     };
     int asked = F::PER * end;  // tiles asked for by the piece's end, F::PER a chunk: k, q, v
     bool unclean = false;      // the last of those chunks is yet to be cleaned
@@ -694,6 +709,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
             asked = F::PER * m + F::PER - 1, unclean = clean;
             break;
           }
+          late(m);
           fetch(1, m, clean);
           if (clean) {
             bool ok = true;
@@ -724,7 +740,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
 #pragma unroll 1
         for (int m = base; m < end; ++m) {
           if (!__all_sync(0xFFFFFFFFu, wait_bar(&sh.bar_out[m & 1], (m >> 1) & 1) &&
-                                           *reinterpret_cast<volatile int*>(&sh.abort) == 0)) break;
+                                           !gone(&sh.abort))) break;
           const int t0 = u.t0 + (m - base) * C;
           if (ln == 0) {
             if (u.n - (m - base) * C >= C && !tab.state) {
@@ -765,6 +781,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
             if (ln == 0) mbar_arrive(&sh.full[2][m % F::ST]);
             continue;
           }
+          if (x == 1) late(m);
           const uint32_t dst = tile(x, m);
           if (x == 0) weights(m, min(C, u.n - (m - base) * C));
           int row[4];  // of tokens ln, ln + 32, ..
@@ -1103,7 +1120,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
       for (int m = base; m < end + (AHEAD ? 1 : 0); ++m) {
         if (m < end) {
           wait_bar(&sh.full[0][m % F::ST], (m / F::ST) & 1);
-          if (__any_sync(0xFFFFFFFFu, timed_out || *reinterpret_cast<volatile int*>(&sh.abort))) break;
+          if (__any_sync(0xFFFFFFFFu, timed_out || gone(&sh.abort))) break;
           convert_k(m, terms_of(tab, left - (AHEAD && m > base ? C : 0)), kAll);
         }
         const int j = AHEAD ? m - 1 : m;
@@ -1133,7 +1150,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         arrive(&sh.bar_k);
 #pragma unroll 1
         for (int m = base; left > 0; ++m, left -= C) {
-          if (__any_sync(0xFFFFFFFFu, timed_out || *reinterpret_cast<volatile int*>(&sh.abort))) break;
+          if (__any_sync(0xFFFFFFFFu, timed_out || gone(&sh.abort))) break;
           if (left > C) {
             full(m + 1);
             convert_k(m + 1, terms_of(tab, left - C), kAll);
@@ -1158,7 +1175,7 @@ __global__ void __launch_bounds__(TcCfg<D, STATES>::NT + 128, D == 64 ? 2 : 1) d
         // At D = 64 all of them leave together there.  At D = 128 only chunks of three terms have that barrier, and after a
         // wait was given up the warps may learn of it on different sides of the first one: the chunks that are left are
         // passed over, their barriers are not.
-        const bool stop = timed_out || *reinterpret_cast<volatile int*>(&sh.abort);
+        const bool stop = timed_out || gone(&sh.abort);
         if (F::SMALL || terms == 3 ? bar_or(1 + (warp & 3), 32 * CG, stop) : (bool)__any_sync(0xFFFFFFFFu, stop)) {
           if (F::SMALL) break;
           timed_out = true;
