@@ -4,13 +4,15 @@
 // The state's bytes bound it: each is read once and written once.  One block per
 // (row, head) holds up to 64 rows' worth of 16-byte loads per column group in
 // flight: thread = (4 value channels, one of RL key-channel lanes), 16 key rows
-// of a lane at a time in registers.  Everything is fp32; only o is rounded.
+// of a lane at a time in registers.  Everything is fp32; only o is rounded.  lambda
+// is applied as hi + lo, as the prompt form does: a rounded one, off by up to
+// 2^-25 the same way at every token, would take the state 1e-4 off in 4000 tokens,
+// where the roundings of the states, which go either way, leave 3e-6.
 // 253 rows, 16 heads of 128/128 (535 MB): 85 to 88 us, 6.1 TB/s, 93% of the measured copy;
 // one row of 6 heads of 32/64: 4.3 us on the device, a launch's time.
 #include <cuda_bf16.h>
 
-#include "../../include/dig.h"
-#include "dig_common.cuh"
+#include "decay_attn.h"
 #include "sm100.cuh"
 
 namespace dig {
@@ -40,6 +42,7 @@ template <typename T, typename TO>
 __global__ void __launch_bounds__(kThreads) decay_step_kernel(const StepArgs a) {
   __shared__ float sk[kMaxD], sq[kMaxD];
   __shared__ float4 part[kThreads];
+  __shared__ float2 slam;
   const int h = blockIdx.x % a.H, b = blockIdx.x / a.H;
   const int G = a.dv >> 2, RL = kThreads / G;  // column groups, key-channel lanes
   const int cg = threadIdx.x % G, rl = threadIdx.x / G;
@@ -71,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) decay_step_kernel(const StepArgs a) 
   }
   float v[4];
   load_row<4>(vp + 4 * cg, v);
-  const float lam = expf(a.g[h]);
+  if (threadIdx.x == kThreads - 1) slam = decay_pow(a.g[h], 1);
   // a slot that an earlier row of the call has belongs to that row
   int taken = 0;
   if (a.slots)
@@ -80,6 +83,7 @@ __global__ void __launch_bounds__(kThreads) decay_step_kernel(const StepArgs a) 
     if (threadIdx.x == 0 && h == 0 && a.status) set_status(a.status, DIG_ERR_INVALID_ARGUMENT);
     return;
   }
+  const float lam = slam.x, low = slam.y;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int r0 = rl; r0 < a.dk; r0 += kBatch * RL) {
     if (r0 != rl) load(r0);
@@ -88,10 +92,10 @@ __global__ void __launch_bounds__(kThreads) decay_step_kernel(const StepArgs a) 
       const int r = r0 + i * RL;
       if (on && r < a.dk) {
         const float kr = sk[r], qr = sq[r];
-        s[i].x = fmaf(lam, s[i].x, kr * v[0]);
-        s[i].y = fmaf(lam, s[i].y, kr * v[1]);
-        s[i].z = fmaf(lam, s[i].z, kr * v[2]);
-        s[i].w = fmaf(lam, s[i].w, kr * v[3]);
+        s[i].x = fmaf(lam, s[i].x, fmaf(low, s[i].x, kr * v[0]));
+        s[i].y = fmaf(lam, s[i].y, fmaf(low, s[i].y, kr * v[1]));
+        s[i].z = fmaf(lam, s[i].z, fmaf(low, s[i].z, kr * v[2]));
+        s[i].w = fmaf(lam, s[i].w, fmaf(low, s[i].w, kr * v[3]));
         acc.x = fmaf(qr, s[i].x, acc.x);
         acc.y = fmaf(qr, s[i].y, acc.y);
         acc.z = fmaf(qr, s[i].z, acc.z);
