@@ -494,7 +494,12 @@ cudaError_t ln_bwd_launch(const LnBwdArgs& a, bool vec, cudaStream_t s, int* blo
   });
 }
 
-bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Whether all of the pointers (NULL too) are multiples of `bytes`.
+template <typename... P>
+bool aligned(size_t bytes, const P*... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & (bytes - 1)) == 0;
+}
+size_t size_of(int dtype) { return dtype == DIG_BF16 ? 2 : 4; }
 
 dig_status ln_fail(dig_status s, const char* msg) {
   set_last_error(msg);
@@ -510,10 +515,11 @@ dig_status ln_check(long long rows, int D, long long x_stride, int dtype, int ou
   return DIG_OK;
 }
 
-// Whether every row of the dense tensors and of x starts at a 16-byte boundary.
+// Whether rows are taken in 16-byte pieces: every row of the dense tensors and of x then starts at a 16-byte boundary if
+// the tensor does.
 bool ln_vec(int D, long long x_stride, int dtype) {
   const int v = dtype == DIG_BF16 ? 8 : 4;
-  return D % v == 0 && x_stride % v == 0;
+  return D <= 8192 && D % v == 0 && x_stride % v == 0;
 }
 
 }  // namespace
@@ -536,10 +542,12 @@ dig_status dig_layer_norm_fwd(const void* x, long long x_stride, const float* we
   if (!(eps >= 0.f)) return ln_fail(DIG_ERR_INVALID_ARGUMENT, "layer norm: eps must be >= 0");
   if (rows == 0) return DIG_OK;
   if (!x || !y) return ln_fail(DIG_ERR_INVALID_ARGUMENT, "layer norm: x and y must be non-NULL");
-  if (!al16(x) || !al16(y) || !al16(weight) || !al16(bias) || !al16(mean) || !al16(rstd))
-    return ln_fail(DIG_ERR_MISALIGNED, "layer norm: a tensor pointer is not 16-byte aligned");
-  const LnArgs a{x, x_stride, weight, bias, eps, y, mean, rstd, rows, D};
   const bool vec = ln_vec(D, x_stride, dtype);
+  if (!aligned(size_of(dtype), x) || !aligned(size_of(out_dtype), y) || !aligned(4, weight, bias, mean, rstd))
+    return ln_fail(DIG_ERR_MISALIGNED, "layer norm: a tensor pointer is not aligned to its elements");
+  if (vec && !aligned(16, x, y, weight, bias))
+    return ln_fail(DIG_ERR_MISALIGNED, "layer norm: rows of 16-byte pieces, but x, y, weight or bias is not 16-byte aligned");
+  const LnArgs a{x, x_stride, weight, bias, eps, y, mean, rstd, rows, D};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == DIG_BF16
                             ? (out_dtype == DIG_BF16 ? ln_fwd_launch<__nv_bfloat16, __nv_bfloat16>(a, vec, s)
@@ -556,9 +564,12 @@ dig_status dig_layer_norm_bwd(const void* x, long long x_stride, const float* we
   if (st != DIG_OK) return st;
   if (rows > 0 && (!x || !mean || !rstd || !dy || !dx))
     return ln_fail(DIG_ERR_INVALID_ARGUMENT, "layer norm backward: x, mean, rstd, dy and dx must be non-NULL");
-  if (!al16(x) || !al16(weight) || !al16(mean) || !al16(rstd) || !al16(dy) || !al16(dx) || !al16(dweight) ||
-      !al16(dbias) || !al16(workspace))
-    return ln_fail(DIG_ERR_MISALIGNED, "layer norm backward: a tensor pointer is not 16-byte aligned");
+  const bool vec = ln_vec(D, x_stride, dtype);
+  if (!aligned(size_of(dtype), x, dy) || !aligned(size_of(out_dtype), dx) || !aligned(4, weight, mean, rstd, dweight, dbias))
+    return ln_fail(DIG_ERR_MISALIGNED, "layer norm backward: a tensor pointer is not aligned to its elements");
+  if ((vec && !aligned(16, x, dy, dx, weight)) || !aligned(16, workspace))
+    return ln_fail(DIG_ERR_MISALIGNED,
+                   "layer norm backward: the workspace, or with rows of 16-byte pieces x, dy, dx or weight, is not 16-byte aligned");
   const bool par = dweight || dbias;
   if (par && !workspace) return ln_fail(DIG_ERR_INVALID_ARGUMENT, "layer norm backward: dweight and dbias need a workspace");
   if (par && workspace_bytes < dig_layer_norm_workspace_bytes(rows, D))
@@ -571,7 +582,6 @@ dig_status dig_layer_norm_bwd(const void* x, long long x_stride, const float* we
   int blocks = 0;
   cudaError_t e = cudaSuccess;
   if (rows > 0) {
-    const bool vec = ln_vec(D, x_stride, dtype);
     e = dtype == DIG_BF16 ? (out_dtype == DIG_BF16 ? ln_bwd_launch<__nv_bfloat16, __nv_bfloat16>(a, vec, s, &blocks)
                                                    : ln_bwd_launch<__nv_bfloat16, float>(a, vec, s, &blocks))
                           : (out_dtype == DIG_BF16 ? ln_bwd_launch<float, __nv_bfloat16>(a, vec, s, &blocks)

@@ -404,7 +404,9 @@ dig_status dig_decay_attn_step(const void *q, const void *k, const void *v, long
  *   y = (x - mean) * rstd * weight + bias,   rstd = 1 / sqrt(var + eps), var over D
  *   x  [rows, D] dtype, rows x_stride elements apart (>= D);  y [rows, D] out_dtype, dense
  *   weight, bias [D] fp32 or NULL (ones, zeros);  mean, rstd [rows] fp32 or NULL
- * Any D >= 1 and any stride; 16-byte accesses where D and the stride allow them. */
+ * Any D >= 1 and any stride, tensors aligned to their elements.  Where D and the stride
+ * are multiples of 16 bytes of x's type and D is at most 8192, rows are taken in 16-byte
+ * pieces, and x, y, weight and bias have to be 16-byte aligned (else DIG_ERR_MISALIGNED). */
 dig_status dig_layer_norm_fwd(const void *x, long long x_stride, const float *weight, const float *bias,
                               float eps, void *y, float *mean, float *rstd, long long rows, int D, int dtype,
                               int out_dtype, void *stream);
@@ -414,7 +416,8 @@ dig_status dig_layer_norm_fwd(const void *x, long long x_stride, const float *we
  *   dy [rows, D] dtype, dense;  dx [rows, D] out_dtype, dense
  *   dweight, dbias [D] fp32 or NULL: sums over the rows (overwritten), added in a fixed
  *   order, so the same from run to run; with either the workspace
- *   (dig_layer_norm_workspace_bytes; any contents) is needed. */
+ *   (dig_layer_norm_workspace_bytes; any contents, 16-byte aligned) is needed.
+ * Alignment as the forward's, of x, dy, dx and weight. */
 dig_status dig_layer_norm_bwd(const void *x, long long x_stride, const float *weight, const float *mean,
                               const float *rstd, const void *dy, void *dx, float *dweight, float *dbias,
                               long long rows, int D, int dtype, int out_dtype, void *workspace,
