@@ -257,8 +257,10 @@ struct LnBwdArgs {
   int D;
 };
 
+// Two blocks of 256 threads an SM, 128 registers, at D from 2049 to 4096: with 163 and one block 8191 x 4096 fp32 values take
+// 90 us, so 70.  Elsewhere the compiler's own choice (0: no bound) is the better one.
 template <typename T, typename TO, int V, int NV, int TPR>
-__global__ void __launch_bounds__(threads_of<TPR>) ln_bwd_kernel(const LnBwdArgs a) {
+__global__ void __launch_bounds__(threads_of<TPR>, (V > 1 && TPR == 256 ? 2 : 0)) ln_bwd_kernel(const LnBwdArgs a) {
   constexpr int NT = threads_of<TPR>, RPB = NT / TPR;
   __shared__ float red[4 * NT / 32];
   extern __shared__ float part[];  // [RPB][D], only for RPB > 1
@@ -313,17 +315,23 @@ __global__ void __launch_bounds__(threads_of<TPR>) ln_bwd_kernel(const LnBwdArgs
     }
     fetch(row + step);
     float s[2] = {0.f, 0.f};
+    // Past D g and w g are 0, but xh = (0 - mean) rstd need not be finite, nor 0 times it 0.  It is not only where all values
+    // of the row are the mean itself (one that is not is off by 2^-25 of it at least, and |xh| is at most sqrt(D)).  So the
+    // mean of those columns is taken as 0; or, where 512 threads have no register to spare for that, the sum of such a row,
+    // whose xh are all 0, is.
+    constexpr bool ZERO = TPR < 512;
 #pragma unroll
-    for (int n = 0; n < NV * V; ++n) {  // past D both g and w g are 0
-      xh[n] = (xh[n] - mean) * rstd;
+    for (int n = 0; n < NV * V; ++n) {
+      xh[n] = (xh[n] - (ZERO && (n / V * TPR + tr) * V >= a.D ? 0.f : mean)) * rstd;
       gw[n] = fmaf(g[n], xh[n], gw[n]);
       gb[n] += g[n];
       g[n] *= w[n];
       s[0] += g[n];
       s[1] = fmaf(g[n], xh[n], s[1]);
     }
+    const bool flat = !ZERO && !isfinite(mean * rstd);
     row_sums<TPR, 2>(s, red, turn);
-    const float s1 = s[0] * inv_d, s2 = s[1] * inv_d;
+    const float s1 = s[0] * inv_d, s2 = flat ? 0.f : s[1] * inv_d;
     if (row >= a.rows) continue;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
