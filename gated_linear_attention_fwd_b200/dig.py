@@ -376,6 +376,13 @@ def _row_stride(t, name, inner, size):
     return size if step is None else step
 
 
+def _fits(*sizes):
+    """Refuses sizes that an int does not hold (the call would get their low 32 bits)."""
+    for n in sizes:
+        if n > 0x7FFFFFFF:
+            raise ValueError("a size of %d is more than the library takes" % n)
+
+
 def _call(fn, where, dev, stream, *args):
     """fn(*args, stream) with device `dev` current (launches go to the current device), its status checked."""
     if dev < 0:
@@ -400,6 +407,7 @@ def decay_attn_workspace_bytes(B, H, L, d_k, d_v, dtype=torch.bfloat16, packed=F
 def new_decay_attn_workspace(B, H, L, d_k, d_v, dtype=torch.bfloat16, packed=False, backward=False,
                              device="cuda") -> torch.Tensor:
     """A zero-filled workspace (uint8) for dig_decay_attn_fwd / dig_decay_attn_bwd; packed: B sequences in L rows."""
+    _fits(B, H, L, d_k, d_v)
     n = decay_attn_workspace_bytes(B, H, L, d_k, d_v, dtype, packed, backward)
     if n == 0:
         raise ValueError("unsupported shape for the head-decay attention")
@@ -427,6 +435,7 @@ def _decay_shape(q, k, v, o, cu_seqlens, grid_h, grid_w):
         B, L = lead
         if grid_h is None and grid_w is None:
             grid_h, grid_w = 1, L
+    _fits(B, H, L, dk, dv)
     return B, H, L, dk, dv, grid_h, grid_w, _tokens(q, "q", H, dk), _tokens(k, "k", H, dk), _tokens(v, "v", H, dv)
 
 
@@ -441,6 +450,7 @@ def dig_decay_attn_fwd(q, k, v, log_decay, o, workspace, grid_h=None, grid_w=Non
     if slots is not None:
         pool = S0 if S0 is not None else S_final
         n = pool.shape[0] if pool is not None else 0
+        _fits(n)
     state = (n, H, dk, dv)
     f32 = torch.float32
     _call(lib.dig_decay_attn_fwd, "dig_decay_attn_fwd", dev, stream,
@@ -478,6 +488,7 @@ def dig_decay_attn_step(q, k, v, log_decay, S, o, slots=None, scale=1.0, device_
             v.dtype is not dt or k.get_device() != dev or v.get_device() != dev:
         raise ValueError("q, k [B, H, d_k] and v [B, H, d_v] must agree in shape, dtype and device")
     dv, n = vshape[2], S.shape[0]
+    _fits(B, H, dk, dv, n)
     _call(lib.dig_decay_attn_step, "dig_decay_attn_step", dev, stream,
           q.data_ptr(), k.data_ptr(), v.data_ptr(), _tokens(q, "q", H, dk), _tokens(k, "k", H, dk),
           _tokens(v, "v", H, dv), _dense(log_decay, "log_decay", (H,), _F32, dev), scale,
@@ -492,6 +503,7 @@ def _rows(x):
     if not shape or shape[-1] == 0:
         raise ValueError("x must be [..., D] with dense rows")
     D = shape[-1]
+    _fits(D)
     if x.is_contiguous():
         return D, x.numel() // D, D
     if D > 1 and x.stride(-1) != 1:
@@ -512,6 +524,7 @@ def dig_layer_norm_fwd(x, y, weight=None, bias=None, eps=1e-5, mean=None, rstd=N
 
 def new_layer_norm_workspace(rows, D, device="cuda") -> torch.Tensor:
     """A workspace (uint8) for dig_layer_norm_bwd with dw or db."""
+    _fits(D)
     return torch.empty(int(lib.dig_layer_norm_workspace_bytes(rows, D)), dtype=torch.uint8, device=device)
 
 
