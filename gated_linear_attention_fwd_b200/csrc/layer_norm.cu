@@ -519,7 +519,8 @@ dig_status ln_check(long long rows, int D, long long x_stride, int dtype, int ou
   if (x_stride < D) return ln_fail(DIG_ERR_INVALID_ARGUMENT, "layer norm: x_stride must be at least D");
   if ((dtype != DIG_F32 && dtype != DIG_BF16) || (out_dtype != DIG_F32 && out_dtype != DIG_BF16))
     return ln_fail(DIG_ERR_INVALID_ARGUMENT, "layer norm: dtype / out_dtype not DIG_F32 or DIG_BF16");
-  if (rows >= (1ll << 40) / x_stride) return ln_fail(DIG_ERR_INVALID_ARGUMENT, "layer norm: tensor too large");
+  // (columns are counted in int, past D by a block's step)
+  if (D > (1 << 30) || rows >= (1ll << 40) / x_stride) return ln_fail(DIG_ERR_INVALID_ARGUMENT, "layer norm: tensor too large");
   return DIG_OK;
 }
 

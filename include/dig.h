@@ -404,7 +404,7 @@ dig_status dig_decay_attn_step(const void *q, const void *k, const void *v, long
  *   y = (x - mean) * rstd * weight + bias,   rstd = 1 / sqrt(var + eps), var over D
  *   x  [rows, D] dtype, rows x_stride elements apart (>= D);  y [rows, D] out_dtype, dense
  *   weight, bias [D] fp32 or NULL (ones, zeros);  mean, rstd [rows] fp32 or NULL
- * Any D >= 1 and any stride, tensors aligned to their elements.  Where D and the stride
+ * Any D from 1 to 2^30 and any stride, tensors aligned to their elements.  Where D and the stride
  * are multiples of 16 bytes of x's type and D is at most 8192, rows are taken in 16-byte
  * pieces, and x, y, weight and bias have to be 16-byte aligned (else DIG_ERR_MISALIGNED). */
 dig_status dig_layer_norm_fwd(const void *x, long long x_stride, const float *weight, const float *bias,

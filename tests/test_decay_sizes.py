@@ -31,3 +31,10 @@ def test_the_binding_refuses_what_an_int_does_not_hold():
     for i, call in enumerate(calls):
         with pytest.raises(ValueError, match="more than the library takes"):
             call()
+
+
+def test_layer_norm_refuses_widths_past_its_counters():
+    D = (1 << 30) + 1
+    assert dig.lib.dig_layer_norm_fwd(1024, D, None, None, 1e-5, 1024, None, None, 1, D, 1, 1, None) == dig.DIG_ERR_INVALID_ARGUMENT
+    assert dig.lib.dig_layer_norm_bwd(1024, D, None, 1024, 1024, 1024, 1024, None, None, 1, D, 1, 1, None, 0, None) == \
+        dig.DIG_ERR_INVALID_ARGUMENT
