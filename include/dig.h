@@ -348,15 +348,25 @@ dig_status dig_block_activation(void *x, long long n, int kind, void *stream);
  *               sequence b uses state slots[b]; a negative one starts from zero and
  *               leaves no state.  Slots must differ (negative ones aside).
  * d_k and d_v are multiples of 4 up to 128, strides multiples of 4 elements; else
- * DIG_ERR_UNSUPPORTED.  q, k and v are aligned to four elements, the rest to 16 bytes.  Values have to be finite: a NaN or infinity may reach other
- * tokens of its own sequence (never another sequence's).  Offsets and slots live on the
- * device: offsets that leave 0 .. L or descend (clamped to the rows; what such a call leaves
- * in o and S_final is undefined, and some of it may not be written), a slot of n_slots or
- * more or one that an earlier sequence has (then taken as negative) set
- * DIG_ERR_INVALID_ARGUMENT in the workspace's status word.  The workspace (dig_decay_attn_workspace_bytes, zero-filled
- * before the first use, and again after DIG_ERR_DEVICE_TIMEOUT) is scratch of one call at a time.  o overlaps no input
- * (blocks read tokens that others have answered).  Results do not depend on
- * what shares the call and are the same from run to run. */
+ * DIG_ERR_UNSUPPORTED.  q, k and v are aligned to four elements, the rest to 16 bytes.
+ * Values have to be finite: a NaN or infinity may reach other tokens of its own sequence
+ * (never another sequence's).  Offsets and slots live on the device: offsets that leave
+ * 0 .. L or descend (clamped to the rows; what such a call leaves in o and S_final is
+ * undefined, and some of it may not be written), a slot of n_slots or more or one that an
+ * earlier sequence has (then taken as negative) set DIG_ERR_INVALID_ARGUMENT in the
+ * workspace's status word.  The workspace (dig_decay_attn_workspace_bytes, zero-filled
+ * before the first use, and again after DIG_ERR_DEVICE_TIMEOUT) is scratch of one call of
+ * dig_decay_attn_fwd or _bwd at a time, and of no other operator (it keeps counters there
+ * that have to be zero).  o overlaps no input (blocks read tokens that others have answered).
+ * The same call gives the same bits from run to run.  Where a sequence is cut among blocks
+ * depends on the whole call (B, H, L, the lengths before it), so in other company the same
+ * sequence may differ by roundings: the fp32 state's, and what follows from them below.
+ * fp32 and mixed types are computed in fp32 throughout.  With bf16 in and out products are
+ * summed in fp32 and the state is held in fp32, but where it meets q it is rounded to bf16:
+ * a relative 2^-8 of each of its values at most, as o's own rounding (bf16 in with fp32 out
+ * does without, at the fp32 path's speed).  q k^T under its mask and the decayed k enter
+ * their products as two bf16 terms (2^-16 at most); what goes into S_final as three (exact
+ * to fp32), unless it decays below 2^-10 by then. */
 dig_status dig_decay_attn_fwd(const void *q, const void *k, const void *v, long long q_stride,
                               long long k_stride, long long v_stride, const float *log_decay, float scale,
                               const int *cu_seqlens, const float *S0, float *S_final, const int *slots,
@@ -370,8 +380,9 @@ dig_status dig_decay_attn_fwd(const void *q, const void *k, const void *v, long 
  *   dS_final   [B, H, d_k, d_v] fp32 or NULL (zero)
  *   dq, dk     [rows, H, d_k] out_dtype;  dv [rows, H, d_v] out_dtype; dense; rows of no
  *              sequence are left as they were
- *   dS0        [B, H, d_k, d_v] fp32 or NULL: the gradient of S0; it overlaps no input
- * Nothing of the forward is kept: the states are computed again. */
+ *   dS0        [B, H, d_k, d_v] fp32 or NULL: the gradient of S0
+ * dq, dk, dv and dS0 overlap no input and not each other.  Nothing of the forward is kept: the
+ * states are computed again.  Roundings as the forward's, with dS0 for S_final. */
 dig_status dig_decay_attn_bwd(const void *q, const void *k, const void *v, long long q_stride,
                               long long k_stride, long long v_stride, const float *log_decay, float scale,
                               const int *cu_seqlens, const float *S0, const void *dO, const float *dS_final,
