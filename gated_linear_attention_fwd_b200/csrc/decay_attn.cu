@@ -25,6 +25,7 @@ struct Cut {
   int seg;        // tokens of a segment
   int nps;        // segments of a sequence of L tokens (whole sequences only)
   int total;      // segment slots of the call
+  int kept;       // segment states of a problem and head
   bool multi;     // whether a sequence may have several segments
   size_t states;  // floats of all problems' segment states
 };
@@ -47,6 +48,8 @@ Cut cut_of(int B, int H, int L, int dk, int dv, int chunk, int per_sm, bool pack
     r.total = B + L / r.seg;
     r.nps = 1;
     r.multi = L > r.seg;
+    // sequences of one segment have none, and one of n > seg tokens has at most 2 (n / seg)
+    r.kept = 2ll * (L / r.seg) < r.total ? 2 * (L / r.seg) : r.total;
   } else {
     double best = 0;
     const int most = L > 0 ? (L + chunk - 1) / chunk : 1;
@@ -63,9 +66,10 @@ Cut cut_of(int B, int H, int L, int dk, int dv, int chunk, int per_sm, bool pack
       }
     }
     r.total = B * r.nps;
+    r.kept = r.total;
     r.multi = r.nps > 1;
   }
-  r.states = r.multi ? (size_t)nprob * r.total * H * r.D * r.D : 0;
+  r.states = r.multi ? (size_t)nprob * r.kept * H * r.D * r.D : 0;
   return r;
 }
 
@@ -214,7 +218,8 @@ dig_status launch(DecayArgs& a, int nprob, int dk, int dv, void* ws, int dtype, 
     const Cut c = cut_for(a.B, a.H, a.L, dk, dv, a.cu != nullptr, nprob);
     a.seg = c.seg;
     a.nps = c.nps;
-    a.segst_problem = (long long)c.total * a.H * c.D * c.D;
+    a.states = c.kept;
+    a.segst_problem = (long long)c.kept * a.H * c.D * c.D;
     e = launch_decay_f32(a, nprob, c.total, c.multi, c.D, dtype, out_dtype, s);
   }
   return e == cudaSuccess ? DIG_OK : attn_fail(DIG_ERR_CUDA, cudaGetErrorString(e));

@@ -70,6 +70,7 @@ struct DecayArgs {
   int B, H, L, Hg, Wg;
   int seg;        // tokens of a segment
   int nps;        // segments of a sequence of L tokens (without cu)
+  int states;     // segment states of a problem and head
   DecayDeal deal;
   uint32_t* flag;     // [block] a block's state has been handed over (left zero)
   uint32_t* counter;  // blocks started, blocks done (left zero)
@@ -86,6 +87,7 @@ struct DecayUnit {
   int first, len;  // the sequence's first row and length
   int t0, n;       // the segment's first scan position and its tokens
   int slot;        // state of the sequence, -1: none
+  int first_state; // the sequence's first segment among the segment states (those of several segments have any)
 };
 
 // Row of scan position t of unit u's sequence.
@@ -116,9 +118,9 @@ __device__ __forceinline__ int decay_slot(const DecayArgs& a, int b) {
 
 // The unit of segment slot `sidx` of the call; every lane of the calling warp
 // gets it.  False: the call has fewer segments, or the unit's sequence reaches past
-// the call's slots, one per block of gridDim.x.  Only sequences that overlap, as
-// those of descending offsets do, can: they come to more tokens than the rows that
-// the slots are counted for, and are left out whole.
+// the call's slots, one per block of gridDim.x, or past its segment states.  Only
+// sequences that overlap, as those of descending offsets do, can: they come to more
+// tokens than the rows that both are counted for, and are left out whole.
 __device__ __forceinline__ bool decay_unit(const DecayArgs& a, int sidx, DecayUnit& u) {
   const int lane = threadIdx.x & 31;
   if (!a.cu) {
@@ -127,8 +129,9 @@ __device__ __forceinline__ bool decay_unit(const DecayArgs& a, int sidx, DecayUn
     u.nseg = a.nps;
     u.first = u.b * a.L;
     u.len = a.L;
+    u.first_state = u.b * a.nps;
   } else {
-    int base = 0;
+    int base = 0, states = 0;
     bool found = false;
     for (int b0 = 0; b0 < a.B && !found; b0 += 32) {
       int lo = 0, hi = 0, ns = 0;
@@ -136,11 +139,11 @@ __device__ __forceinline__ bool decay_unit(const DecayArgs& a, int sidx, DecayUn
         decay_bounds(a, b0 + lane, lo, hi);
         ns = max(1, (hi - lo + a.seg - 1) / a.seg);
       }
-      int inc = ns;
+      int inc = ns, st = ns > 1 ? ns : 0;
 #pragma unroll
       for (int m = 1; m < 32; m <<= 1) {
-        const int x = __shfl_up_sync(0xFFFFFFFFu, inc, m);
-        if (lane >= m) inc += x;
+        const int x = __shfl_up_sync(0xFFFFFFFFu, inc, m), y = __shfl_up_sync(0xFFFFFFFFu, st, m);
+        if (lane >= m) inc += x, st += y;
       }
       const unsigned has = __ballot_sync(0xFFFFFFFFu, base + inc > sidx);
       if (has) {
@@ -150,11 +153,13 @@ __device__ __forceinline__ bool decay_unit(const DecayArgs& a, int sidx, DecayUn
         u.i = sidx - base - (__shfl_sync(0xFFFFFFFFu, inc, src) - u.nseg);
         u.first = __shfl_sync(0xFFFFFFFFu, lo, src);
         u.len = __shfl_sync(0xFFFFFFFFu, hi, src) - u.first;
+        u.first_state = states + __shfl_sync(0xFFFFFFFFu, st, src) - u.nseg;
         found = true;
       }
       base += __shfl_sync(0xFFFFFFFFu, inc, 31);
+      states += __shfl_sync(0xFFFFFFFFu, st, 31);
     }
-    if (!found || sidx - u.i + u.nseg > (int)gridDim.x) return false;
+    if (!found || sidx - u.i + u.nseg > (int)gridDim.x || (u.nseg > 1 && u.first_state + u.nseg > a.states)) return false;
   }
   u.t0 = u.i * a.seg;
   u.n = min(a.seg, u.len - u.t0);

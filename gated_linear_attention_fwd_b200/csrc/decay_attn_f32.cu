@@ -86,11 +86,10 @@ __global__ void __launch_bounds__(256, D == 128 ? 2 : 3) decay_f32_kernel(const 
     }
   }
   float* seg_base = a.segst + blockIdx.z * a.segst_problem;
-  const int seg0 = blockIdx.x - u.i;  // segment slot of the sequence's first segment
-  auto seg_state = [&](int sidx) { return seg_base + ((size_t)sidx * a.H + h) * (D * D); };
+  auto seg_state = [&](int i) { return seg_base + ((size_t)(u.first_state + i) * a.H + h) * (D * D); };  // of the sequence's segment i
   if (!STATES && u.nseg > 1) {
     if (u.i == 0) {  // the copy of S0 that the first pass left (S0 may be overwritten by the last segment)
-      const float* s0 = seg_state(seg0 + u.nseg - 1);
+      const float* s0 = seg_state(u.nseg - 1);
 #pragma unroll
       for (int i = 0; i < TC; ++i)
 #pragma unroll
@@ -102,7 +101,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 2 : 3) decay_f32_kernel(const 
       const float2 w = decay_pow(g, a.seg);
 #pragma unroll 1
       for (int m = 0; m < u.i; ++m) {
-        const float* ls = seg_state(seg0 + m);
+        const float* ls = seg_state(m);
 #pragma unroll
         for (int i = 0; i < TC; ++i)
 #pragma unroll
@@ -117,7 +116,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 2 : 3) decay_f32_kernel(const 
     }
   }
   if (STATES && u.i == 0) {
-    float* s0 = seg_state(seg0 + u.nseg - 1);  // the last segment's place is free: it leaves no state there
+    float* s0 = seg_state(u.nseg - 1);  // the last segment's place is free: it leaves no state there
 #pragma unroll
     for (int i = 0; i < TC; ++i)
 #pragma unroll
@@ -267,7 +266,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 2 : 3) decay_f32_kernel(const 
     }
   }
   if (STATES) {
-    float* out = seg_state(blockIdx.x);
+    float* out = seg_state(u.i);
 #pragma unroll
     for (int i = 0; i < TC; ++i)
 #pragma unroll
