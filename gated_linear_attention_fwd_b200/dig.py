@@ -376,11 +376,10 @@ def _row_stride(t, name, inner, size):
     return size if step is None else step
 
 
-def _fits(*sizes):
-    """Refuses sizes that an int does not hold (the call would get their low 32 bits)."""
-    for n in sizes:
-        if n > 0x7FFFFFFF:
-            raise ValueError("a size of %d is more than the library takes" % n)
+def _fits(sizes):
+    """Refuses sizes, or'ed together, of which an int does not hold one (the call would get its low 32 bits)."""
+    if sizes > 0x7FFFFFFF:
+        raise ValueError("a size is more than the library takes (2^31 - 1)")
 
 
 def _call(fn, where, dev, stream, *args):
@@ -407,7 +406,7 @@ def decay_attn_workspace_bytes(B, H, L, d_k, d_v, dtype=torch.bfloat16, packed=F
 def new_decay_attn_workspace(B, H, L, d_k, d_v, dtype=torch.bfloat16, packed=False, backward=False,
                              device="cuda") -> torch.Tensor:
     """A zero-filled workspace (uint8) for dig_decay_attn_fwd / dig_decay_attn_bwd; packed: B sequences in L rows."""
-    _fits(B, H, L, d_k, d_v)
+    _fits(B | H | L | d_k | d_v)
     n = decay_attn_workspace_bytes(B, H, L, d_k, d_v, dtype, packed, backward)
     if n == 0:
         raise ValueError("unsupported shape for the head-decay attention")
@@ -435,7 +434,7 @@ def _decay_shape(q, k, v, o, cu_seqlens, grid_h, grid_w):
         B, L = lead
         if grid_h is None and grid_w is None:
             grid_h, grid_w = 1, L
-    _fits(B, H, L, dk, dv)
+    _fits(B | H | L | dk | dv)
     return B, H, L, dk, dv, grid_h, grid_w, _tokens(q, "q", H, dk), _tokens(k, "k", H, dk), _tokens(v, "v", H, dv)
 
 
@@ -488,7 +487,7 @@ def dig_decay_attn_step(q, k, v, log_decay, S, o, slots=None, scale=1.0, device_
             v.dtype is not dt or k.get_device() != dev or v.get_device() != dev:
         raise ValueError("q, k [B, H, d_k] and v [B, H, d_v] must agree in shape, dtype and device")
     dv, n = vshape[2], S.shape[0]
-    _fits(B, H, dk, dv, n)
+    _fits(B | H | dk | dv | n)
     _call(lib.dig_decay_attn_step, "dig_decay_attn_step", dev, stream,
           q.data_ptr(), k.data_ptr(), v.data_ptr(), _tokens(q, "q", H, dk), _tokens(k, "k", H, dk),
           _tokens(v, "v", H, dv), _dense(log_decay, "log_decay", (H,), _F32, dev), scale,
