@@ -112,7 +112,6 @@ Cut cut_for(int B, int H, int L, int dk, int dv, bool packed, int nprob) {
 struct Deal {
   DecayDeal d;
   int D;
-  bool multi;     // whether a unit may be cut
   size_t states;  // floats
 };
 Deal deal_for(int B, int H, int L, int dk, int dv, bool packed, int nprob) {
@@ -143,9 +142,8 @@ Deal deal_for(int B, int H, int L, int dk, int dv, bool packed, int nprob) {
     }
   }
   if (packed) r.d.gran = 1;
-  r.multi = cuttable && r.d.gran == 1 && !r.d.handoff;
-  r.d.joined = r.multi;
-  r.states = r.d.handoff || r.multi ? (size_t)2 * r.d.grid * r.D * r.D : 0;
+  r.d.joined = cuttable && r.d.gran == 1 && !r.d.handoff;
+  r.states = r.d.handoff || r.d.joined ? (size_t)2 * r.d.grid * r.D * r.D : 0;
   return r;
 }
 
@@ -213,7 +211,7 @@ dig_status launch(DecayArgs& a, int nprob, int dk, int dv, void* ws, int dtype, 
     const unsigned long long limit = spin_limit_ns();
     a.short_wait = limit != 0 && limit < kSpinLimitNs;
     a.late_chunk = limit < 1000 ? (int)limit - 1 : -1;
-    e = launch_decay_tc(a, d.multi, d.D, s);
+    e = launch_decay_tc(a, d.D, s);
   } else {
     const Cut c = cut_for(a.B, a.H, a.L, dk, dv, a.cu != nullptr, nprob);
     a.seg = c.seg;

@@ -275,9 +275,9 @@ __device__ __forceinline__ float2 decay_pow(float g, long long i) {
   return make_float2(hi, isfinite(hi) ? static_cast<float>(p - hi) : 0.f);
 }
 
-// Launches of the two passes (states: only where a sequence has more than one segment).
+// The launches of a call (FP32 pipes: two passes where a sequence may have several segments, `multi`).
 cudaError_t launch_decay_f32(const DecayArgs& a, int nprob, int nseg_total, bool multi, int D, int dtype, int out_dtype,
                              cudaStream_t s);
-cudaError_t launch_decay_tc(const DecayArgs& a, bool multi, int D, cudaStream_t s);
+cudaError_t launch_decay_tc(const DecayArgs& a, int D, cudaStream_t s);
 
 }  // namespace dig

@@ -1,15 +1,16 @@
 // decay_attn_tc.cu -- head-decay linear attention on the tensor core (bf16 inputs
 // and outputs).
 //
-// One block walks a segment of one (sequence, head) in chunks of 128 tokens; per
+// One block walks its share of the (sequence, head) units in chunks of 128 tokens; per
 // chunk (n tokens, entry state S, the problem's factors a, b, c):
 //   P  = q k^T,            P[t][s] <- a lambda^(t-s) P[t][s] for s <= t, else 0
 //   dS = khat^T v,         khat_s = b lambda^(n-1-s) k_s
 //   O1 = q S,              O2 = P v,      o[t] = c lambda^(t+1) O1[t] + O2[t]
 //   S  = lambda^n S + dS
 // all four products by tcgen05.mma with fp32 accumulators in tensor memory.  One
-// warp issues them, three more fetch a tile each, and the rest (4 warps per 32
-// lanes at D = 128, 2 at D = 64, so that a thread holds 32 columns of S, dS and O
+// warp issues them; with TMA one fetches the tiles, one stores outputs and one plans,
+// token by token three fetch a tile each and one of these plans too; the rest (4 warps
+// per 32 lanes at D = 128, 2 at D = 64, so that a thread holds 32 columns of S, dS and O
 // either way) do what is between the products:
 //   - q, k, v tiles (raw bf16, exact) come two chunks deep (three in the first pass) into 128-byte-swizzled
 //     tiles of 64 channels, by TMA (boxes of whole rows, or of runs of a grid
@@ -23,8 +24,8 @@
 //     0 to 1 is in range);
 //   - S lives in fp32 registers (one key channel per lane) and is left in shared
 //     memory as one bf16 term, the second operand of q S: off by at most half a
-//     bf16 step, as the output's own rounding is (a second term has no room beside
-//     two chunks of tiles).  lambda^n is applied as hi + lo and dS is summed apart
+//     bf16 step, as the output's own rounding is (at D = 128 a second term has no room
+//     beside two chunks of tiles; fp32 outputs take the FP32 pipes, which do without).  lambda^n is applied as hi + lo and dS is summed apart
 //     from S: a tensor-core accumulator that carried S through the sequence would
 //     cut a little off it at every addition;
 //   - khat^T (lane = channel) goes to tensor memory through transposing matrix
@@ -48,8 +49,14 @@
 // rest.  A chunk whose state needs three terms takes 7800, one walked for its state
 // alone 3000, a piece's start 4000, a block's 10000.  At 32 x 64 a chunk takes 8000 in
 // each of two blocks: its chain.  Whole calls: 16382 packed tokens, 16 heads of
-// 128/128, 115 us (2.5 TB/s); 2 x 12544 tokens, 6 heads of 32/64, 54 us; backward of
-// 4 x 4096 tokens, 16 heads of 128/128, 220 us (2.2 TB/s).
+// 128/128, 112 to 119 us (2.5 TB/s); 2 x 12544 tokens, 6 heads of 32/64, 53 us; backward of
+// 4 x 4096 tokens, 16 heads of 128/128, 217 to 229 us (2.2 TB/s).  Token by token 16384
+// tokens of 16 heads of 36/72 take 211 us, their backward 608.
+//
+// Every wait on a barrier or a flag is bounded.  After one was given up the roles pass over
+// what is left of the piece without leaving each other at its barriers, wait for the loads,
+// stores and products in flight and leave together; the status says so, and flags and
+// counters end at zero as ever.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -1312,10 +1319,10 @@ cudaError_t run(const DecayArgs& a, cudaStream_t s) {
 }
 
 template <int D, int FETCH>
-cudaError_t passes(const DecayArgs& a, bool multi, cudaStream_t s) {
+cudaError_t passes(const DecayArgs& a, cudaStream_t s) {
   cudaError_t e;
-  if (multi && (e = run<D, true, FETCH>(a, s)) != cudaSuccess) return e;
-  if (multi && a.deal.joined &&
+  if (a.deal.joined && (e = run<D, true, FETCH>(a, s)) != cudaSuccess) return e;
+  if (a.deal.joined &&
       (e = launch_pdl(decay_join_kernel<D>, dim3(a.B * a.H * a.deal.nprob, D * D / 1024), dim3(256), 0, s, a)) != cudaSuccess)
     return e;
   return run<D, false, FETCH>(a, s);
@@ -1323,12 +1330,12 @@ cudaError_t passes(const DecayArgs& a, bool multi, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_decay_tc(const DecayArgs& a, bool multi, int D, cudaStream_t s) {
+cudaError_t launch_decay_tc(const DecayArgs& a, int D, cudaStream_t s) {
   auto go = [&](auto d) {
     constexpr int DD = decltype(d)::value;
-    return a.fetch == kFetchRows   ? passes<DD, kFetchRows>(a, multi, s)
-           : a.fetch == kFetchCols ? passes<DD, kFetchCols>(a, multi, s)
-                                   : passes<DD, kFetchTokens>(a, multi, s);
+    return a.fetch == kFetchRows   ? passes<DD, kFetchRows>(a, s)
+           : a.fetch == kFetchCols ? passes<DD, kFetchCols>(a, s)
+                                   : passes<DD, kFetchTokens>(a, s);
   };
   return D == 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
 }

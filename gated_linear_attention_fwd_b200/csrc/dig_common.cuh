@@ -11,7 +11,9 @@ namespace dig {
 
 // Launches a kernel with programmatic stream serialization: it may be scheduled
 // while the previous kernel of the stream is still running, and every kernel of
-// this library waits (griddepcontrol.wait) before its first global memory access.
+// this library waits (griddepcontrol.wait) before its first global memory access -- but for
+// the head-decay attention's second pass, which fetches inputs of the call before it waits
+// for the first: that one started after everything before the call had ended.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                        Args... args) {

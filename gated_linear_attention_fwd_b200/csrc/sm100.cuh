@@ -97,7 +97,7 @@ __device__ __forceinline__ void named_bar(int id, int count) {
 // Kernels of one stream are launched with programmatic stream serialization: a
 // kernel may be scheduled while the kernel before it is still running, runs its
 // prologue (TMEM allocation, barrier setup, tables computed from its arguments;
-// no global memory), and then waits here until every kernel it depends on has
+// no global memory that a kernel it may overlap writes), and then waits here until every kernel it depends on has
 // completed and its memory is visible.  A no-op for a plain launch.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Lets the next kernel of the stream be scheduled.  Called only after this
