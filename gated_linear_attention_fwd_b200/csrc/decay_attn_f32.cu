@@ -13,7 +13,7 @@
 //
 // Shared-memory reads bound the products of 32 tokens (q S, P v: 5 reads of 16 bytes
 // for 16 multiply-adds of a thread), a block's chain the small calls: 4 x 1024 tokens,
-// 16 heads of 128/128, 296 us, 14.5 TFLOP/s of the recurrent form's operations (one
+// 16 heads of 128/128, 297 us, 14.5 TFLOP/s of the recurrent form's operations (one
 // block an SM, with padded rows: 347 us); 8 x 256 tokens, 6 heads of 64/64, 22 us.
 #include <cuda_bf16.h>
 

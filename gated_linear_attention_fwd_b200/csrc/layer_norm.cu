@@ -12,8 +12,8 @@
 // gradients are summed per thread over the block's rows, then over the block's
 // rows of threads, and the blocks' partial rows by a second kernel, all in a
 // fixed order (no atomics: the same bits from run to run).
-// Forward 16384 x 4096 bf16 48 us (5.6 TB/s, 85% of the measured copy), backward 8191 x 4096 fp32 69 us
-// (5.8 TB/s, 89%); rows that 16-byte vectors do not fit run at 2 to 4 TB/s (a value at a time: the loads'
+// Forward 16384 x 4096 bf16 48 us (5.6 TB/s, 85% of the measured copy), backward 8191 x 4096 fp32 69 to 71 us
+// (5.8 TB/s, 88%); rows that 16-byte vectors do not fit run at 2 to 4 TB/s (a value at a time: the loads'
 // and the reductions' latency).
 #include <cuda_bf16.h>
 
